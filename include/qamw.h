@@ -402,6 +402,60 @@ QAMW_API int qamw_decode_gemm(const qamw_matrix *m, const uint16_t *d_x, int nto
 QAMW_API int qamw_decode_gemv_noalloc(const qamw_matrix *m, const uint16_t *d_x, int batch,
                                       uint16_t *d_y, int32_t *d_status, void *stream);
 
+/* ------------------------------------------------- 8-bit integers (W8A8) */
+/* The 8-bit baseline that the paper's bit rates are set against (weights and
+ * activations in 8-bit integers with per-channel smoothing scales s_j from
+ * qamw_channel_scales): x W^T = (x / s) (W * s)^T, each factor stored as
+ *   q (int8, row-major, 16B-aligned) and one fp32 scale per row,
+ * row [j] ~ scale * q[j].  For a row with values v_j (fp32, below) and
+ * a = max |v_j|:
+ *   q_j = rint(v_j * (127 / a)) (ties to even, so |q_j| <= 127), scale = a / 127,
+ * every operation rounded once to fp32; a row with a < 2^-100 (a row of zeros)
+ * gives q = 0, scale = 0, and a row with a NaN or Inf among its values gives
+ * q = 0, scale = NaN (flagged NONFINITE), which the product carries to that
+ * row's outputs alone.  d and d_in are multiples of 64 up to 32768; a count of
+ * 0 rows is a no-op.  Inputs and outputs may not overlap, except where stated.
+ * None of these calls needs a workspace.  d_chan_scale: binary16 [d],
+ * 16B-aligned, non-zero; NULL stands for s = 1.
+ *
+ * qamw_int8_encode_weights: v_j = W_ij * s_j for each of d_out rows (dtype
+ *   QAMW_DTYPE_F32 or _BF16); d_q [d_out][d_in], d_row_scale [d_out].  The
+ *   weight it stands for is d_row_scale[i] * q[i][j] / s_j. */
+QAMW_API int qamw_int8_encode_weights(const void *d_W, int dtype, int d_out, int d_in,
+                                      const uint16_t *d_chan_scale, int8_t *d_q,
+                                      float *d_row_scale, int32_t *d_status, void *stream);
+
+/* qamw_int8_encode_tokens: v_j = x_tj * (1 / s_j) for each of ntok tokens;
+ *   d_q [ntok][d], d_tok_scale [ntok]. */
+QAMW_API int qamw_int8_encode_tokens(const void *d_x, int dtype, int ntok, int d,
+                                     const uint16_t *d_chan_scale, int8_t *d_q,
+                                     float *d_tok_scale, int32_t *d_status, void *stream);
+
+/* qamw_rmsnorm_int8: root-mean-square norm with the residual's addition and its
+ *   output in 8 bits.  h = x + residual, rounded to the type of x (dtype; x,
+ *   residual, gain and sum share it) and written to d_sum; without a residual
+ *   (d_residual and d_sum both NULL) h = x.  The token's values are
+ *   h_j / sqrt(mean h^2 + eps) * gain_j / s_j: q from v_j = h_j * (gain_j / s_j)
+ *   as above (the common factor cancels), d_tok_scale = (a / 127) /
+ *   sqrt(mean h^2 + eps) with the sum of squares in fp32.
+ *   d_gain [d], 16B-aligned; eps >= 2^-126.  d_sum may be d_x or d_residual
+ *   (the residual stream updated in place).  Errors: QAMW_ERR_INVALID for one of
+ *   d_residual and d_sum without the other, or eps out of range. */
+QAMW_API int qamw_rmsnorm_int8(const void *d_x, const void *d_residual, int dtype,
+                               const void *d_gain, float eps, int ntok, int d,
+                               const uint16_t *d_chan_scale, void *d_sum, int8_t *d_q,
+                               float *d_tok_scale, int32_t *d_status, void *stream);
+
+/* qamw_int8_gemm: Y[t][i] = d_tok_scale[t] * d_row_scale[i] * sum_j x[t][j] w[i][j],
+ *   the sum an exact 32-bit integer (all 256 values of int8 are allowed).
+ *   d_x [ntok][d_in], 0 <= ntok <= 65536; d_w [d_out][d_in]; d_y [ntok][d_out]
+ *   in dtype (QAMW_DTYPE_BF16 or _F32), rounded once from
+ *   float(sum) * (tok_scale * row_scale).  The result does not depend on how
+ *   the work is split.  Flags: TIMEOUT. */
+QAMW_API int qamw_int8_gemm(const int8_t *d_x, const float *d_tok_scale, int ntok,
+                            const int8_t *d_w, const float *d_row_scale, int d_out, int d_in,
+                            void *d_y, int dtype, int32_t *d_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

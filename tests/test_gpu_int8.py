@@ -1,0 +1,453 @@
+"""The 8-bit (W8A8) operators on the GPU against plain numpy forms.
+
+Row encoders and the norm: the 8-bit values equal those of the stated fp32 steps
+exactly, and the 64-bit mathematics within half a unit; scales within the
+roundings counted below.  Product: each output within its three fp32 roundings
+(float(sum), the product of the scales, their product) and the output's own."""
+import numpy as np
+import pytest
+import torch
+
+from tests import int8_ref as ref
+from vector_quantization_codec_b200 import qamw
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+T = {"bf16": torch.bfloat16, "f32": torch.float32}
+U32, UBF16 = ref.U32, ref.UBF16
+
+
+def f32(t):
+    return t.detach().float().cpu().numpy()
+
+
+def status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def values(rows, d, kind, seed, scale=1.0):
+    g = np.random.default_rng(seed)
+    x = g.standard_normal((rows, d)) * scale
+    x[:, g.random(d) < 0.01] *= 20
+    return torch.from_numpy(x.astype(np.float32)).to(T[kind]).to(DEV)
+
+
+def chan_scale(d, seed):
+    return torch.from_numpy(np.random.default_rng(seed).lognormal(0, 0.5, d).astype(np.float16)).to(DEV)
+
+
+def check_rows(q, scale, h, c, s, gain, divide, eps=None):
+    """q exactly; scale against 64 bits: v, a: <= 2 roundings, a / 127: 1 (encoders: <= 3).  The
+    norm adds 1 / sqrt(sum / d + eps): the sum of squares of positive terms is off by at most one
+    rounding per addition on a term's path, 32 in the thread, 10 in the two shuffle trees, and 1
+    of the square; with / d and + eps 45, halved by the root, then root, reciprocal and product:
+    23 + 3, in all <= 29."""
+    hf = f32(h)
+    q_want, scale_want, _ = ref.rows32(hf, c)
+    np.testing.assert_array_equal(q.cpu().numpy(), q_want)
+    got = scale.cpu().numpy().astype(np.float64)
+    u64, scale64 = ref.rows64(hf, s, gain, divide, eps)
+    n = 3 if eps is None else 29
+    assert (np.abs(got - scale64) <= n * U32 * scale64 * (1 + 1e-6)).all()
+    assert np.abs(q_want - u64).max() <= 0.5 + 5e-5
+    if eps is None:
+        np.testing.assert_array_equal(scale.cpu().numpy(), scale_want)
+
+
+WIDTHS = [64, 128, 192, 512, 1024, 1088, 2048, 4096, 5120, 8192, 11008, 13824, 16448, 24640, 32768]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d", WIDTHS)
+def test_encoders(d, kind):
+    rows = 19
+    x = values(rows, d, kind, d)
+    x[rows - 1] = 0
+    s = chan_scale(d, d + 1)
+    for fn, divide, sc in ((qamw.qamw_int8_encode_weights, False, s),
+                           (qamw.qamw_int8_encode_tokens, True, s),
+                           (qamw.qamw_int8_encode_tokens, True, None)):
+        st = status()
+        q, scale = fn(x, sc, status=st)
+        assert st.item() == 0
+        sn = None if sc is None else sc.cpu().numpy()
+        check_rows(q, scale, x, ref.factors32(d, sn, None, divide), sn, None, divide)
+        assert scale[-1].item() == 0 and not q[-1].any()
+
+
+@pytest.mark.parametrize("rows", [1, 2, 7, 8, 9, 149, 3001])
+@pytest.mark.parametrize("d", [64, 1024, 2048])
+def test_encoder_row_counts(rows, d):
+    x = values(rows, d, "bf16", rows)
+    q, scale = qamw.qamw_int8_encode_tokens(x)
+    check_rows(q, scale, x, ref.factors32(d), None, None, True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("d", WIDTHS)
+def test_rmsnorm(d, residual, kind):
+    rows, eps = 13, 1e-5
+    x = values(rows, d, kind, d)
+    x[2] = 0
+    res = values(rows, d, kind, d + 7, 3.0) if residual else None
+    if residual:
+        res[2] = 0
+    gain = (1 + 0.2 * values(1, d, kind, 3)[0].clamp(-3, 3))
+    for s in (None, chan_scale(d, 4)):
+        st = status()
+        out = qamw.qamw_rmsnorm_int8(x, gain, eps, residual=res, chan_scale=s, status=st)
+        assert st.item() == 0
+        h = x
+        if residual:
+            h, out = out[0], out[1:]
+            assert torch.equal(h, (x.float() + res.float()).to(x.dtype))
+        sn = None if s is None else s.cpu().numpy()
+        check_rows(*out, h, ref.factors32(d, sn, f32(gain), True), sn, f32(gain), True, eps)
+        assert out[1][2].item() == 0 and not out[0][2].any()
+
+
+@pytest.mark.parametrize("rows,d", [(1, 4096), (300, 64), (1000, 2048), (2, 32768)])
+def test_rmsnorm_updates_the_residual_stream_in_place(rows, d):
+    for alias in ("x", "residual"):
+        x, res = values(rows, d, "bf16", 1), values(rows, d, "bf16", 2)
+        gain = torch.ones(d, dtype=torch.bfloat16, device=DEV)
+        want = qamw.qamw_rmsnorm_int8(x, gain, residual=res)
+        got = qamw.qamw_rmsnorm_int8(x, gain, residual=res, sum_out=x if alias == "x" else res)
+        assert got[0].data_ptr() == (x if alias == "x" else res).data_ptr()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_rows_with_nan_or_inf_are_flagged_and_stay_alone():
+    for d in (256, 4096):
+        x = values(6, d, "f32", 8)
+        clean, _ = qamw.qamw_int8_encode_tokens(x)
+        x[1, 3] = float("nan")
+        x[4, d - 1] = -float("inf")
+        for fn in (lambda st: qamw.qamw_int8_encode_tokens(x, status=st),
+                   lambda st: qamw.qamw_int8_encode_weights(x, status=st),
+                   lambda st: qamw.qamw_rmsnorm_int8(x, torch.ones(d, device=DEV), status=st)):
+            st = status()
+            q, scale = fn(st)
+            assert st.item() == qamw.QAMW_STATUS_NONFINITE
+            assert torch.isnan(scale).tolist() == [False, True, False, False, True, False]
+            assert not q[1].any() and not q[4].any()
+            keep = [0, 2, 3, 5]
+            assert torch.equal(q[keep], clean[keep])
+        # the product of such a token is NaN, and only that token's
+        xq, xs = qamw.qamw_int8_encode_tokens(x)
+        wq, ws = qamw.qamw_int8_encode_weights(values(70, d, "f32", 9))
+        y = qamw.qamw_int8_gemm(xq, xs, wq, ws)
+        assert torch.isnan(y).all(dim=1).tolist() == torch.isnan(xs).tolist()
+        assert torch.isnan(y).any(dim=1).tolist() == torch.isnan(xs).tolist()
+
+
+def test_extreme_magnitudes():
+    """Rows near the ends of the range: values whose squares overflow or underflow, rows that are
+    only just rows of zeros."""
+    d, eps = 2048, 1e-6
+    base = f32(values(1, d, "f32", 4))[0] / 100
+    rows = np.stack([base * np.float32(v) for v in (1e37, 1e25, 1e18, 1.0, 1e-18, 1e-25, 2.0 ** -98)]
+                    + [np.full(d, 2.0 ** -101, np.float32), np.full(d, 2.0 ** -100, np.float32)])
+    x = torch.from_numpy(rows.astype(np.float32)).to(DEV)
+    q, scale = qamw.qamw_int8_encode_tokens(x)
+    q_want, scale_want, _ = ref.rows32(rows, ref.factors32(d))
+    np.testing.assert_array_equal(q.cpu().numpy(), q_want)
+    np.testing.assert_array_equal(scale.cpu().numpy(), scale_want)
+    assert not q[7].any() and scale[7].item() == 0 and (q[8] == 127).all()
+    st = status()
+    q, scale = qamw.qamw_rmsnorm_int8(x, torch.ones(d, device=DEV), eps, status=st)
+    assert st.item() == 0
+    np.testing.assert_array_equal(q.cpu().numpy(), q_want)
+    _, scale64 = ref.rows64(rows, None, None, True, eps)
+    keep = [i for i in range(9) if i != 7]
+    got = scale.cpu().numpy().astype(np.float64)
+    # the rescaled sum of squares rounds three more times than the 29 of check_rows
+    assert (np.abs(got - scale64) <= 32 * U32 * scale64 + 2.0 ** -149)[keep].all()
+
+
+# ---------------------------------------------------------------- product
+
+def ints(rows, d, seed, full=False):
+    g = torch.Generator().manual_seed(seed)
+    lo = -128 if full else -127
+    return torch.randint(lo, 128, (rows, d), generator=g, dtype=torch.int8).to(DEV)
+
+
+def scales(n, seed):
+    return torch.from_numpy(np.random.default_rng(seed).lognormal(-3, 1, n).astype(np.float32)).to(DEV)
+
+
+def check_gemm(xq, xs, wq, ws, dtype, y=None):
+    st = status()
+    got = qamw.qamw_int8_gemm(xq, xs, wq, ws, y=y, dtype=dtype, status=st)
+    assert st.item() == 0, qamw.status_string(st.item())
+    assert got.shape == (xq.shape[0], wq.shape[0]) and got.dtype == dtype
+    a = xq.double() @ wq.double().T  # exact: |sum| <= 2^29
+    want = a * (xs.double()[:, None] * ws.double()[None, :])
+    tol = 3 * U32 + (UBF16 if dtype is torch.bfloat16 else 0)
+    bad = (got.double() - want).abs() > tol * want.abs() * (1 + 1e-5)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:5].tolist())
+    return got
+
+
+TOKENS = [1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 31, 33, 64, 65, 100, 128, 129, 200, 256, 257, 511, 1000]
+
+
+@pytest.mark.parametrize("ntok", TOKENS)
+def test_gemm_token_counts(ntok):
+    for d_out, d_in in ((300, 1024), (129, 192)):
+        check_gemm(ints(ntok, d_in, ntok), scales(ntok, 1), ints(d_out, d_in, 3), scales(d_out, 2),
+                   torch.bfloat16)
+
+
+@pytest.mark.parametrize("d_out", [1, 2, 7, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 1001, 5003])
+def test_gemm_output_widths(d_out):
+    for ntok, d_in in ((1, 256), (6, 512), (40, 320), (140, 128), (300, 64)):
+        check_gemm(ints(ntok, d_in, d_out), scales(ntok, 5), ints(d_out, d_in, 7), scales(d_out, 6),
+                   torch.float32 if d_out % 2 else torch.bfloat16)
+
+
+@pytest.mark.parametrize("d_in", [64, 128, 192, 256, 448, 1088, 4096, 4160, 11008, 13824, 32768])
+def test_gemm_depths(d_in):
+    for ntok, d_out in ((1, 130), (3, 64), (20, 200), (150, 300), (520, 260)):
+        check_gemm(ints(ntok, d_in, 11), scales(ntok, 8), ints(d_out, d_in, d_in), scales(d_out, 9),
+                   torch.float32)
+
+
+@pytest.mark.parametrize("shape", [(1, 4096, 4096), (1, 11008, 4096), (7, 4096, 11008),
+                                   (16, 4096, 11008), (64, 5120, 5120), (100, 4096, 11008),
+                                   (333, 11008, 4096), (777, 13824, 5120), (2048, 4096, 4096)],
+                         ids=str)
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_gemm_layer_shapes(shape, kind):
+    ntok, d_out, d_in = shape
+    check_gemm(ints(ntok, d_in, 1), scales(ntok, 2), ints(d_out, d_in, 3), scales(d_out, 4), T[kind])
+
+
+@pytest.mark.parametrize("ntok", [1, 12, 100, 300])
+def test_gemm_extreme_sums(ntok):
+    """Sums of +-2^29 (all 256 values of int8 are allowed) and exact zeros."""
+    d_in, d_out = 32768, 140
+    for xv, wv in ((-128, -128), (-128, 127), (127, 127), (0, -128)):
+        xq = torch.full((ntok, d_in), xv, dtype=torch.int8, device=DEV)
+        wq = torch.full((d_out, d_in), wv, dtype=torch.int8, device=DEV)
+        y = check_gemm(xq, torch.ones(ntok, device=DEV), wq, torch.ones(d_out, device=DEV), torch.float32)
+        assert (y == float(xv * wv * d_in)).all()
+    check_gemm(ints(ntok, d_in, 2, full=True), scales(ntok, 3), ints(d_out, d_in, 4, full=True),
+               scales(d_out, 5), torch.bfloat16)
+
+
+@pytest.mark.parametrize("ntok,d_out,kind", [(1, 77, "bf16"), (5, 77, "f32"), (13, 129, "bf16"),
+                                             (70, 131, "bf16"), (130, 300, "f32"), (300, 257, "bf16")])
+def test_gemm_writes_its_outputs_alone(ntok, d_out, kind):
+    """y inside a larger buffer, at an odd element offset: what stands around it stays."""
+    d_in, pad = 256, 1
+    buf = torch.full((pad + ntok * d_out + 4096,), -7.0, dtype=T[kind], device=DEV)
+    y = buf[pad:pad + ntok * d_out].view(ntok, d_out)
+    check_gemm(ints(ntok, d_in, 1), scales(ntok, 2), ints(d_out, d_in, 3), scales(d_out, 4), T[kind], y)
+    assert (buf[:pad] == -7).all() and (buf[pad + ntok * d_out:] == -7).all()
+
+
+@pytest.mark.parametrize("ntok", [1, 9, 128, 400])
+def test_gemm_is_the_same_every_time_and_reads_only_its_rows(ntok):
+    d_in, d_out = 1024, 333
+    big_x, big_w = ints(ntok + 300, d_in, 1), ints(d_out + 300, d_in, 2)
+    xs, ws = scales(ntok + 300, 3), scales(d_out + 300, 4)
+    want = qamw.qamw_int8_gemm(big_x[:ntok].clone(), xs[:ntok].clone(), big_w[:d_out].clone(),
+                               ws[:d_out].clone())
+    for _ in range(3):
+        y = qamw.qamw_int8_gemm(big_x[:ntok], xs[:ntok], big_w[:d_out], ws[:d_out])
+        assert torch.equal(y, want)
+
+
+def test_empty_calls():
+    x = torch.empty((0, 128), dtype=torch.bfloat16, device=DEV)
+    q, s = qamw.qamw_int8_encode_tokens(x)
+    assert q.shape == (0, 128) and s.shape == (0,)
+    h, q, s = qamw.qamw_rmsnorm_int8(x, torch.ones(128, dtype=torch.bfloat16, device=DEV), residual=x)
+    assert h.shape == (0, 128) and q.shape == (0, 128)
+    assert qamw.qamw_int8_gemm(q, s, ints(5, 128, 1), scales(5, 1)).shape == (0, 5)
+    assert qamw.qamw_int8_gemm(ints(5, 128, 1), scales(5, 1), q, s).shape == (5, 0)
+
+
+def test_wrappers_refuse_what_does_not_fit():
+    x = values(4, 128, "bf16", 1)
+    with pytest.raises(ValueError):
+        qamw.qamw_int8_encode_tokens(x.to(torch.float16))
+    with pytest.raises(ValueError):
+        qamw.qamw_int8_encode_tokens(x[:, :64])                     # strided
+    with pytest.raises(ValueError):
+        qamw.qamw_int8_encode_tokens(x, chan_scale(64, 1))          # too short
+    with pytest.raises(ValueError):
+        qamw.qamw_int8_encode_tokens(x, chan_scale(128, 1).cpu())   # elsewhere
+    with pytest.raises(ValueError):
+        qamw.qamw_int8_encode_tokens(x, chan_scale(128, 1).float())
+    with pytest.raises(ValueError):
+        qamw.qamw_int8_encode_tokens(x, q=torch.empty((3, 128), dtype=torch.int8, device=DEV))
+    with pytest.raises(qamw.QamwError):
+        qamw.qamw_int8_encode_tokens(values(4, 96, "bf16", 1))
+    gain = torch.ones(128, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        qamw.qamw_rmsnorm_int8(x, gain.float())
+    with pytest.raises(ValueError):
+        qamw.qamw_rmsnorm_int8(x, gain, sum_out=x)
+    with pytest.raises(ValueError):
+        qamw.qamw_rmsnorm_int8(x, gain, residual=x[:2])
+    with pytest.raises(qamw.QamwError):
+        qamw.qamw_rmsnorm_int8(x, gain, eps=0.0)
+    xq, xs, wq, ws = ints(4, 128, 1), scales(4, 1), ints(8, 128, 2), scales(8, 2)
+    for bad in ((xq, xs, wq[:, :64], ws), (xq, xs[:3], wq, ws), (xq, xs, wq, ws.double()),
+                (xq.to(torch.uint8), xs, wq, ws), (xq, xs, wq.cpu(), ws), (xq[0], xs, wq, ws)):
+        with pytest.raises(ValueError):
+            qamw.qamw_int8_gemm(*bad)
+    with pytest.raises(ValueError):
+        qamw.qamw_int8_gemm(xq, xs, wq, ws, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        qamw.qamw_int8_gemm(xq, xs, wq, ws, y=torch.empty((4, 9), dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError):
+        qamw.qamw_int8_gemm(xq, xs, wq, ws, status=torch.zeros(1, device=DEV))
+
+
+# ---------------------------------------------------------------- together
+
+def mlp(x, res, gain, wg, wu, wd, s_in, s_mid, status=None, stream=None):
+    """Norm, gate and up projections, silu, down projection of a W8A8 layer."""
+    h, q, ts = qamw.qamw_rmsnorm_int8(x, gain, residual=res, chan_scale=s_in, status=status, stream=stream)
+    g = qamw.qamw_int8_gemm(q, ts, *wg, status=status, stream=stream)
+    u = qamw.qamw_int8_gemm(q, ts, *wu, status=status, stream=stream)
+    return h, g, u
+
+
+def layer(d, f, ntok, seed):
+    w = [values(f, d, "bf16", seed, 0.02), values(f, d, "bf16", seed + 1, 0.02),
+         values(d, f, "bf16", seed + 2, 0.02)]
+    s_in, s_mid = chan_scale(d, seed + 3), chan_scale(f, seed + 4)
+    enc = [qamw.qamw_int8_encode_weights(w[0], s_in), qamw.qamw_int8_encode_weights(w[1], s_in),
+           qamw.qamw_int8_encode_weights(w[2], s_mid)]
+    x, res = values(ntok, d, "bf16", seed + 5), values(ntok, d, "bf16", seed + 6)
+    gain = (1 + 0.1 * values(1, d, "bf16", seed + 7)[0].clamp(-3, 3))
+    return w, enc, s_in, s_mid, x, res, gain
+
+
+def full(x, res, gain, enc, s_in, s_mid):
+    h, g, u = mlp(x, res, gain, enc[0], enc[1], enc[2], s_in, s_mid)
+    a = torch.nn.functional.silu(g.float()) * u.float()
+    q, ts = qamw.qamw_int8_encode_tokens(a.to(torch.bfloat16), s_mid)
+    return h, a, q, ts, qamw.qamw_int8_gemm(q, ts, *enc[2])
+
+
+def check_linear(y, n, W, q, ts, enc, s):
+    """y against n W^T in 64 bits.  Each factor is off by at most half a unit of its row (and 5e-5
+    for the fp32 roundings): with x' = n / s and W' = W s, |x' - ts q| <= 0.50005 ts and
+    |W' - ws wq| <= 0.50005 ws, so |n W^T - product| <= 0.50005 (ts sum |W'| + ws sum |ts q|),
+    plus the product's own roundings."""
+    s, ts, wq, ws = s.double(), ts.double()[:, None], enc[0].double(), enc[1].double()[None, :]
+    ys = ts * q.double() @ wq.T * ws
+    off = 0.50005 * (ts * (W.double() * s).abs().sum(1)[None, :] + ws * (ts * q.double().abs()).sum(1)[:, None])
+    want = n @ W.double().T
+    assert ((y.double() - want).abs() <= off + 2 * (UBF16 + 3 * U32) * ys.abs()).all()
+
+
+@pytest.mark.parametrize("ntok", [1, 3, 37, 200])
+def test_mlp_of_a_w8a8_layer(ntok):
+    """The operators one after another, as a layer uses them: norm, gate and up products, the
+    activation encoded, down product; each product against the unquantised weights and inputs."""
+    d, f = 512, 1408
+    w, enc, s_in, s_mid, x, res, gain = layer(d, f, ntok, 20)
+    h, q, ts = qamw.qamw_rmsnorm_int8(x, gain, residual=res, chan_scale=s_in)
+    hd = (x.double() + res.double()).to(torch.bfloat16).double()
+    assert torch.equal(h.double(), hd)
+    n = hd * torch.rsqrt((hd * hd).mean(1, keepdim=True) + 1e-5) * gain.double()
+    g, u = qamw.qamw_int8_gemm(q, ts, *enc[0]), qamw.qamw_int8_gemm(q, ts, *enc[1])
+    check_linear(g, n, w[0], q, ts, enc[0], s_in)
+    check_linear(u, n, w[1], q, ts, enc[1], s_in)
+    a = (torch.nn.functional.silu(g.float()) * u.float()).to(torch.bfloat16)
+    q, ts = qamw.qamw_int8_encode_tokens(a, s_mid)
+    check_linear(qamw.qamw_int8_gemm(q, ts, *enc[2]), a.double(), w[2], q, ts, enc[2], s_mid)
+
+
+def test_captured_graphs_and_streams():
+    """Two captured graphs (which share nothing but their inputs) replayed in turn and on two
+    streams at once give the eager results; so does a call on a stream that is not current."""
+    d, f, ntok = 512, 1408, 5
+    _, enc, s_in, s_mid, x, res, gain = layer(d, f, ntok, 40)
+    want = full(x, res, gain, enc, s_in, s_mid)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            full(x, res, gain, enc, s_in, s_mid)
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(full(x, res, gain, enc, s_in, s_mid))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for o in outs:
+        for t in o:
+            t.zero_()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(a):
+            graphs[0].replay()
+        with torch.cuda.stream(b):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(p, q) for p, q in zip(o, want))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (s, s.cuda_stream):
+        h, g, u = mlp(x, res, gain, enc[0], enc[1], enc[2], s_in, s_mid, stream=stream)
+        s.synchronize()
+        assert torch.equal(h, want[0])
+        h2, g2, u2 = mlp(x, res, gain, enc[0], enc[1], enc[2], s_in, s_mid)
+        torch.cuda.synchronize()
+        assert torch.equal(g, g2) and torch.equal(u, u2)
+
+
+def test_new_inputs_in_a_captured_graph():
+    """A replay reads what its inputs hold then: other tokens, other weights."""
+    xq, xs, wq, ws = ints(3, 512, 1), scales(3, 1), ints(200, 512, 2), scales(200, 2)
+    y = torch.empty((3, 200), device=DEV)
+    qamw.qamw_int8_gemm(xq, xs, wq, ws, y=y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qamw.qamw_int8_gemm(xq, xs, wq, ws, y=y)
+    for seed in (5, 6):
+        xq.copy_(ints(3, 512, seed))
+        wq.copy_(ints(200, 512, seed + 10))
+        xs.copy_(scales(3, seed))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, check_gemm(xq, xs, wq, ws, torch.float32))
+
+
+def test_product_feeds_the_decode_products():
+    """In one stream with the codec's own kernels, each launched before the one ahead ends: the
+    8-bit product's output as the input of a decode-GEMV and of the prefill product."""
+    from tests.test_gpu_parity import codebook, gpu_encode, weights
+    d, bits = 512, 7
+    cb = codebook(bits)
+    Wt, _ = weights(96, d, 3, "bf16")
+    m, st = gpu_encode(Wt, d, 64, bits, cb, None, 0.0, seed=1)
+    assert st == 0
+    for ntok in (1, 4, 64):
+        xq, xs, wq, ws = ints(ntok, 1024, 1), scales(ntok, 1), ints(d, 1024, 2), scales(d, 2)
+        product = qamw.qamw_decode_gemv if ntok <= 16 else qamw.qamw_decode_gemm
+        y = qamw.qamw_int8_gemm(xq, xs, wq, ws)
+        torch.cuda.synchronize()
+        want = product(m, y)
+        torch.cuda.synchronize()
+        out = torch.zeros_like(y)
+        for _ in range(20):
+            out.zero_()
+            got = product(m, qamw.qamw_int8_gemm(xq, xs, wq, ws, y=out))
+            q, _ = qamw.qamw_int8_encode_tokens(got.repeat(1, 2)[:, :128].contiguous())
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)

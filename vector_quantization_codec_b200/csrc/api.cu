@@ -1,5 +1,6 @@
 // api.cu -- extern "C" entry points of libqamw.so: argument checks, workspace
 // carving and dispatch to the kernels.  Nothing here allocates device memory.
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <mutex>
@@ -139,6 +140,21 @@ int check_matrix(const qamw_matrix* m, bool need_outputs) {
   if (!aligned16(m->sigma) || !aligned16(m->chan_scale)) return QAMW_ERR_ALIGN;
   if (m->prefilter && !aligned16(m->prefilter)) return QAMW_ERR_ALIGN;
   (void)need_outputs;
+  return QAMW_OK;
+}
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Rows of 8-bit codes: shape, dtype and buffers shared by the encoders and the
+// norm (rows == 0 needs no buffers).
+int check_int8_rows(const void* d_x, int dtype, int64_t rows, int d, const uint16_t* d_chan_scale,
+                    const int8_t* d_q, const float* d_scale) {
+  if (dtype != QAMW_DTYPE_F32 && dtype != QAMW_DTYPE_BF16) return QAMW_ERR_INVALID;
+  if (rows < 0 || d <= 0 || d % kE != 0 || d > kMaxDin) return QAMW_ERR_SHAPE;
+  if (rows == 0) return QAMW_OK;
+  if (!d_x || !d_q || !d_scale) return QAMW_ERR_INVALID;
+  if (!aligned16(d_x) || !aligned16(d_q) || !aligned(d_scale, 4)) return QAMW_ERR_ALIGN;
+  if (d_chan_scale && !aligned16(d_chan_scale)) return QAMW_ERR_ALIGN;
   return QAMW_OK;
 }
 
@@ -446,6 +462,54 @@ int qamw_decode_gemm(const qamw_matrix* m, const uint16_t* d_x, int ntok, uint16
   if (!aligned16(d_workspace)) return QAMW_ERR_ALIGN;
   return cuda_rc(launch_decode_gemm(*m, d_x, ntok, d_y, d_workspace, d_status,
                                     static_cast<cudaStream_t>(stream)));
+}
+
+int qamw_int8_encode_weights(const void* d_W, int dtype, int d_out, int d_in,
+                             const uint16_t* d_chan_scale, int8_t* d_q, float* d_row_scale,
+                             int32_t* d_status, void* stream) {
+  const int rc = check_int8_rows(d_W, dtype, d_out, d_in, d_chan_scale, d_q, d_row_scale);
+  if (rc != QAMW_OK || d_out == 0) return rc;
+  return cuda_rc(launch_int8_encode(d_W, dtype, d_out, d_in, d_chan_scale, false, d_q, d_row_scale,
+                                    d_status, static_cast<cudaStream_t>(stream)));
+}
+
+int qamw_int8_encode_tokens(const void* d_x, int dtype, int ntok, int d,
+                            const uint16_t* d_chan_scale, int8_t* d_q, float* d_tok_scale,
+                            int32_t* d_status, void* stream) {
+  const int rc = check_int8_rows(d_x, dtype, ntok, d, d_chan_scale, d_q, d_tok_scale);
+  if (rc != QAMW_OK || ntok == 0) return rc;
+  return cuda_rc(launch_int8_encode(d_x, dtype, ntok, d, d_chan_scale, true, d_q, d_tok_scale,
+                                    d_status, static_cast<cudaStream_t>(stream)));
+}
+
+int qamw_rmsnorm_int8(const void* d_x, const void* d_residual, int dtype, const void* d_gain,
+                      float eps, int ntok, int d, const uint16_t* d_chan_scale, void* d_sum,
+                      int8_t* d_q, float* d_tok_scale, int32_t* d_status, void* stream) {
+  const int rc = check_int8_rows(d_x, dtype, ntok, d, d_chan_scale, d_q, d_tok_scale);
+  if (rc != QAMW_OK) return rc;
+  // not eps >= FLT_MIN also refuses NaN
+  if (!(eps >= FLT_MIN) || !std::isfinite(eps)) return QAMW_ERR_INVALID;
+  if (ntok == 0) return QAMW_OK;
+  if (!d_gain || (d_residual == nullptr) != (d_sum == nullptr)) return QAMW_ERR_INVALID;
+  if (!aligned16(d_gain) || !aligned16(d_residual) || !aligned16(d_sum)) return QAMW_ERR_ALIGN;
+  return cuda_rc(launch_rmsnorm_int8(d_x, d_residual, dtype, d_gain, eps, ntok, d, d_chan_scale,
+                                     d_sum, d_q, d_tok_scale, d_status,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+int qamw_int8_gemm(const int8_t* d_x, const float* d_tok_scale, int ntok, const int8_t* d_w,
+                   const float* d_row_scale, int d_out, int d_in, void* d_y, int dtype,
+                   int32_t* d_status, void* stream) {
+  if (dtype != QAMW_DTYPE_F32 && dtype != QAMW_DTYPE_BF16) return QAMW_ERR_INVALID;
+  if (d_out < 0 || d_in <= 0 || d_in % kE != 0 || d_in > kMaxDin) return QAMW_ERR_SHAPE;
+  if (ntok < 0 || ntok > kMaxTokens) return QAMW_ERR_INVALID;
+  if (ntok == 0 || d_out == 0) return QAMW_OK;
+  if (!d_x || !d_tok_scale || !d_w || !d_row_scale || !d_y) return QAMW_ERR_INVALID;
+  if (!aligned16(d_x) || !aligned16(d_w)) return QAMW_ERR_ALIGN;
+  if (!aligned(d_tok_scale, 4) || !aligned(d_row_scale, 4)) return QAMW_ERR_ALIGN;
+  if (!aligned(d_y, dtype == QAMW_DTYPE_F32 ? 4 : 2)) return QAMW_ERR_ALIGN;
+  return cuda_rc(launch_int8_gemm(d_x, d_tok_scale, ntok, d_w, d_row_scale, d_out, d_in, d_y, dtype,
+                                  d_status, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

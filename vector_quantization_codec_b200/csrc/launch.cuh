@@ -114,5 +114,16 @@ size_t gemv_many_workspace_bytes(const qamw_matrix* ms, int n);
 cudaError_t launch_decode_gemv_many(const qamw_matrix* ms, int n, const uint16_t* const* d_x,
                                     uint16_t* const* d_y, void* d_ws, int32_t* d_status,
                                     cudaStream_t stream);
+// Rows to 8-bit integers: c = s (divide false) or 1 / s.
+cudaError_t launch_int8_encode(const void* d_x, int dtype, int64_t rows, int d,
+                               const uint16_t* d_chan_scale, bool divide, int8_t* d_q,
+                               float* d_scale, int32_t* d_status, cudaStream_t stream);
+cudaError_t launch_rmsnorm_int8(const void* d_x, const void* d_residual, int dtype,
+                                const void* d_gain, float eps, int64_t rows, int d,
+                                const uint16_t* d_chan_scale, void* d_sum, int8_t* d_q,
+                                float* d_scale, int32_t* d_status, cudaStream_t stream);
+cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
+                             const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
+                             int32_t* d_status, cudaStream_t stream);
 
 }  // namespace qamw

@@ -8,10 +8,13 @@ PyTorch fallback, and importing this module fails if the library is missing.
 
 Names follow the C ABI: qamw_train_codebook, qamw_build_prefilter,
 qamw_encode (= qamw_channel_scales + qamw_calibrate_sigma + qamw_encode_rows),
-qamw_decode, qamw_decode_gemv and the size helpers.
+qamw_decode, qamw_decode_gemv and the size helpers; the 8-bit (W8A8) calls are
+qamw_int8_encode_weights, qamw_int8_encode_tokens, qamw_rmsnorm_int8 and
+qamw_int8_gemm.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -52,7 +55,8 @@ EXPORTS = ("qamw_row_bytes", "qamw_default_block", "qamw_bits_per_weight",
            "qamw_decode_gemm",
            "qamw_decode_gemv_noalloc", "qamw_polar_codebook", "qamw_encode_rows_polar",
            "qamw_scalar_codebook", "qamw_encode_rows_scalar",
-           "qamw_normalised_pairs", "qamw_selftest_wait_timeout")
+           "qamw_normalised_pairs", "qamw_selftest_wait_timeout", "qamw_int8_encode_weights",
+           "qamw_int8_encode_tokens", "qamw_rmsnorm_int8", "qamw_int8_gemm")
 
 
 class QamwError(RuntimeError):
@@ -104,6 +108,10 @@ def _load() -> C.CDLL:
         "qamw_encode_rows_scalar": (I, [V, I, C.POINTER(qamw_matrix), V, V]),
         "qamw_normalised_pairs": (I, [V, I, C.POINTER(qamw_matrix), I64, I64, V, V, V]),
         "qamw_selftest_wait_timeout": (I, [C.c_uint, V, V, V]),
+        "qamw_int8_encode_weights": (I, [V, I, I, I, V, V, V, V, V]),
+        "qamw_int8_encode_tokens": (I, [V, I, I, I, V, V, V, V, V]),
+        "qamw_rmsnorm_int8": (I, [V, V, I, V, C.c_float, I, I, V, V, V, V, V, V]),
+        "qamw_int8_gemm": (I, [V, V, I, V, V, I, I, V, I, V, V]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -480,4 +488,155 @@ def qamw_decode_gemv_noalloc(m: EncodedMatrix, x: torch.Tensor, y: torch.Tensor,
     st = m.struct()
     rc = _lib.qamw_decode_gemv_noalloc(C.byref(st), _p(x2), batch, _p(y), _p(status), _s(stream))
     _check("qamw_decode_gemv_noalloc", rc)
+    return y
+
+
+# ------------------------------------------------------- 8-bit integers (W8A8)
+# These wrappers check their tensors (type, shape, contiguity, one device), run
+# on the tensors' own device whichever is current, and allocate what they return
+# on the stream they launch on.
+
+_DTYPE_CODE = {torch.float32: QAMW_DTYPE_F32, torch.bfloat16: QAMW_DTYPE_BF16}
+
+
+def _dense(name: str, t: torch.Tensor, dtype, shape: tuple, device) -> int:
+    """Device address of a tensor that must be dense, of this type and shape, on `device`."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, not {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ' (strided)'}")
+    return t.data_ptr()
+
+
+def _rows_of(name: str, x: torch.Tensor) -> int:
+    """Type code of a [rows, d] input on a GPU."""
+    code = _DTYPE_CODE.get(x.dtype)
+    if code is None or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 or bfloat16 [rows, d] tensor on a "
+                         f"GPU, not {x.dtype} {tuple(x.shape)} on {x.device}")
+    return code
+
+
+class _On:
+    """Makes `device` current, with `stream` (when given) the current stream, for
+    the allocations and the launch inside; `.handle` is the stream to launch on."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.stack = device, stream, None
+
+    def __enter__(self):
+        if self.stream is None and self.device.index == torch.cuda.current_device():
+            self.handle = torch.cuda.current_stream().cuda_stream
+            return self
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(self.device))
+        if self.stream is not None:
+            s = self.stream
+            if not hasattr(s, "cuda_stream"):
+                s = torch.cuda.ExternalStream(int(s), device=self.device)
+            if s.device != self.device:
+                self.stack.close()
+                raise ValueError(f"the stream is on {s.device}, the tensors are on {self.device}")
+            self.stack.enter_context(torch.cuda.stream(s))
+        self.handle = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.close()
+
+
+def _status_ptr(status: torch.Tensor | None, device):
+    return None if status is None else _dense("status", status, torch.int32, status.shape, device)
+
+
+def _int8_encode(fn: str, what: str, x, chan_scale, q, scale, status, stream):
+    code = _rows_of(what, x)
+    rows, d = x.shape
+    dev = x.device
+    with _On(dev, stream) as on:
+        if q is None:
+            q = torch.empty((rows, d), dtype=torch.int8, device=dev)
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=dev)
+        _check(fn, getattr(_lib, fn)(
+            x.data_ptr(), code, rows, d,
+            None if chan_scale is None else _dense("chan_scale", chan_scale, torch.float16, (d,), dev),
+            _dense("q", q, torch.int8, (rows, d), dev),
+            _dense("scale", scale, torch.float32, (rows,), dev), _status_ptr(status, dev), on.handle))
+    return q, scale
+
+
+def qamw_int8_encode_weights(W: torch.Tensor, chan_scale: torch.Tensor | None = None,
+                             q: torch.Tensor | None = None, row_scale: torch.Tensor | None = None,
+                             status: torch.Tensor | None = None, stream=None):
+    """W * chan_scale (W: bf16 or float32 [d_out, d_in], chan_scale: binary16 [d_in]) as int8
+    [d_out, d_in] with one float32 scale per row; returns (q, row_scale)."""
+    return _int8_encode("qamw_int8_encode_weights", "W", W, chan_scale, q, row_scale, status, stream)
+
+
+def qamw_int8_encode_tokens(x: torch.Tensor, chan_scale: torch.Tensor | None = None,
+                            q: torch.Tensor | None = None, tok_scale: torch.Tensor | None = None,
+                            status: torch.Tensor | None = None, stream=None):
+    """x / chan_scale (x: bf16 or float32 [ntok, d]) as int8 [ntok, d] with one float32 scale
+    per token; returns (q, tok_scale)."""
+    return _int8_encode("qamw_int8_encode_tokens", "x", x, chan_scale, q, tok_scale, status, stream)
+
+
+def qamw_rmsnorm_int8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-5,
+                      residual: torch.Tensor | None = None, chan_scale: torch.Tensor | None = None,
+                      sum_out: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                      tok_scale: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                      stream=None):
+    """RMS norm of h = x + residual (x, residual, gain: bf16 or float32 alike), times gain /
+    chan_scale, as int8 [ntok, d] with one float32 scale per token.  Returns (h, q, tok_scale), or
+    (q, tok_scale) without a residual; sum_out (which h is written to) may be x or residual."""
+    code = _rows_of("x", x)
+    rows, d = x.shape
+    dev = x.device
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out needs a residual")
+    with _On(dev, stream) as on:
+        if residual is not None and sum_out is None:
+            sum_out = torch.empty_like(x)
+        if q is None:
+            q = torch.empty((rows, d), dtype=torch.int8, device=dev)
+        if tok_scale is None:
+            tok_scale = torch.empty(rows, dtype=torch.float32, device=dev)
+        _check("qamw_rmsnorm_int8", _lib.qamw_rmsnorm_int8(
+            x.data_ptr(),
+            None if residual is None else _dense("residual", residual, x.dtype, x.shape, dev),
+            code, _dense("gain", gain, x.dtype, (d,), dev), float(eps), rows, d,
+            None if chan_scale is None else _dense("chan_scale", chan_scale, torch.float16, (d,), dev),
+            None if residual is None else _dense("sum_out", sum_out, x.dtype, x.shape, dev),
+            _dense("q", q, torch.int8, (rows, d), dev),
+            _dense("tok_scale", tok_scale, torch.float32, (rows,), dev),
+            _status_ptr(status, dev), on.handle))
+    return (q, tok_scale) if residual is None else (sum_out, q, tok_scale)
+
+
+def qamw_int8_gemm(xq: torch.Tensor, tok_scale: torch.Tensor, wq: torch.Tensor,
+                   row_scale: torch.Tensor, y: torch.Tensor | None = None,
+                   dtype: torch.dtype = torch.bfloat16, status: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """Y = (tok_scale xq) (row_scale wq)^T (xq: int8 [ntok, d_in], wq: int8 [d_out, d_in]) as
+    bf16 or float32 [ntok, d_out], the integer sums exact; dtype is that of y when y is given."""
+    if xq.dim() != 2 or wq.dim() != 2 or not xq.is_cuda:
+        raise ValueError("xq and wq must be int8 [ntok, d_in] and [d_out, d_in] tensors on a GPU")
+    ntok, d_in = xq.shape
+    d_out, dev = wq.shape[0], xq.device
+    if y is not None:
+        dtype = y.dtype
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise ValueError(f"y must be float32 or bfloat16, not {dtype}")
+    with _On(dev, stream) as on:
+        if y is None:
+            y = torch.empty((ntok, d_out), dtype=dtype, device=dev)
+        _check("qamw_int8_gemm", _lib.qamw_int8_gemm(
+            _dense("xq", xq, torch.int8, (ntok, d_in), dev),
+            _dense("tok_scale", tok_scale, torch.float32, (ntok,), dev), ntok,
+            _dense("wq", wq, torch.int8, (d_out, d_in), dev),
+            _dense("row_scale", row_scale, torch.float32, (d_out,), dev), d_out, d_in,
+            _dense("y", y, dtype, (ntok, d_out), dev), code, _status_ptr(status, dev), on.handle))
     return y
