@@ -143,6 +143,9 @@ int check_matrix(const qamw_matrix* m, bool need_outputs) {
   return QAMW_OK;
 }
 
+// Output channels of qamw_int8_gemm: row coordinates of the copies are 32-bit.
+constexpr int kMaxInt8Rows = 1 << 30;
+
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Rows of 8-bit codes: shape, dtype and buffers shared by the encoders and the
@@ -501,7 +504,8 @@ int qamw_int8_gemm(const int8_t* d_x, const float* d_tok_scale, int ntok, const 
                    const float* d_row_scale, int d_out, int d_in, void* d_y, int dtype,
                    int32_t* d_status, void* stream) {
   if (dtype != QAMW_DTYPE_F32 && dtype != QAMW_DTYPE_BF16) return QAMW_ERR_INVALID;
-  if (d_out < 0 || d_in <= 0 || d_in % kE != 0 || d_in > kMaxDin) return QAMW_ERR_SHAPE;
+  if (d_out < 0 || d_out > kMaxInt8Rows || d_in <= 0 || d_in % kE != 0 || d_in > kMaxDin)
+    return QAMW_ERR_SHAPE;
   if (ntok < 0 || ntok > kMaxTokens) return QAMW_ERR_INVALID;
   if (ntok == 0 || d_out == 0) return QAMW_OK;
   if (!d_x || !d_tok_scale || !d_w || !d_row_scale || !d_y) return QAMW_ERR_INVALID;

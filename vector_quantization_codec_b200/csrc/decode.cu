@@ -34,6 +34,7 @@
 
 #include "common.cuh"
 #include "launch.cuh"
+#include "tensor_map.cuh"
 
 namespace qamw {
 namespace {
@@ -324,19 +325,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_decode(const __grid_constant
     bulk_wait_all();
   }
   raise_flag(a.status, flags);
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up once.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
 }
 
 // BF16 [d_out][d_in] seen as [d_out][d_in / 64][64] for tile stores of

@@ -33,6 +33,7 @@
 
 #include "common.cuh"
 #include "launch.cuh"
+#include "tcgen05.cuh"
 
 namespace qamw {
 namespace {
@@ -160,16 +161,6 @@ __global__ void __launch_bounds__(kImgThreads) k_xbar_images(const __nv_bfloat16
 
 // ------------------------------------------------------------ tcgen05 wrappers
 
-// Shared-memory matrix descriptor of a K-major tile with the 128-byte swizzle:
-// start address >> 4 (bits 0-13), leading-dimension offset 16 B (bits 16-29,
-// unused for this layout), stride between 8-row groups 1024 B (bits 32-45),
-// descriptor version 1 (bits 46-47), base offset 0, layout type 2 = 128-byte
-// swizzle (bits 61-63).
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
 // Instruction descriptor of kind::f16 for N tokens: binary16 A and B (formats
 // 0), fp32 accumulator (bits 4-5 = 1), both K-major, N >> 3 at bits 17-22,
 // M >> 4 at bits 24-28.
@@ -198,25 +189,6 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16])
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
-}
-
-// Arrive on the mbarrier once every MMA this thread issued so far has completed.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // 16 consecutive fp32 columns of this warp's 32 tensor-memory lanes.

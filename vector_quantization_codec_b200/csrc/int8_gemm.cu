@@ -1,23 +1,46 @@
 // int8_gemm.cu -- product of 8-bit integers with a scale per token and per
-// output channel:
+// output channel, on the fifth-generation tensor cores (tcgen05.mma kind::i8,
+// exact 32-bit accumulators in tensor memory):
 //   Y[t][i] = T(float(sum_j xq[t][j] wq[i][j]) * (x_scale_t * w_scale_i)).
-// The sum is an exact 32-bit integer (|sum| <= 128 * 128 * 32768 = 2^29), so no
-// order of summation changes a result.
+// The sum is an exact integer (|sum| <= 128 * 128 * 32768 = 2^29), so no tile,
+// split or order of summation changes a result.
+//
+// The weights' rows are M of the MMA (lane of tensor memory = output channel)
+// and the tokens are N (column): N follows the token count in steps of 16 or
+// 32, and the 32 lanes of an epilogue warp store 32 consecutive outputs of a
+// token whatever d_out is.
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.cuh"
 
 namespace qamw {
 namespace {
 
-constexpr int kSimpleTile = 64;
+constexpr int kRowsM = 128;           // output channels per CTA
+constexpr int kChunk = 128;           // bytes of a row per stage: one swizzled line
+constexpr uint32_t kTileA = kRowsM * kChunk;
+constexpr int kMaxStages = 12;
+constexpr int kEpiWarps = 4;          // warps 0-3: one tensor-memory lane quarter each
+constexpr int kMmaWarp = 4;           // owner of the tensor memory; lane 0 issues the MMAs
+constexpr int kCopyWarp = 5;          // lane 0 issues the copies
+constexpr int kThreads = 6 * 32;
 
 struct Int8GemmArgs {
-  const int8_t* x;
   const float* xs;
-  const int8_t* w;
   const float* ws;
   void* y;
-  int ntok, d_out, d_in;
+  int32_t* status;
+  int64_t tiles;   // (row tile, token tile) pairs, token tiles fastest
+  int ntok, d_out;
+  int chunks;      // of 128 bytes along d_in
+  int tail;        // 32-byte steps of the last chunk (2 or 4)
+  int nt;          // tokens per tile
+  int tok_tiles;
+  int stages;
+  int splits;      // CTAs (a cluster) that share a tile's chunks; 1: persistent over tiles
 };
 
 __device__ __forceinline__ void put(float* y, int64_t at, float v) { y[at] = v; }
@@ -25,45 +48,410 @@ __device__ __forceinline__ void put(__nv_bfloat16* y, int64_t at, float v) {
   y[at] = __float2bfloat16_rn(v);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_int8_gemm(const Int8GemmArgs a) {
-  __shared__ int xs[kSimpleTile][17], ws[kSimpleTile][17];
-  const int64_t i0 = (int64_t)blockIdx.x * kSimpleTile;
-  const int t0 = blockIdx.y * kSimpleTile;
-  const int ti = threadIdx.x & 15, tt = threadIdx.x >> 4;
-  int acc[4][4] = {};
+// Address of this CTA's shared address `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ int lds_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+               : "memory");
+}
+
+// Box of `map` at (column x, row y) into this CTA's shared memory; completion on
+// the barrier at `bar` (CG 2: a shared::cluster address, the leader's barrier).
+template <int CG>
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                         uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+// Instruction descriptor of kind::i8: signed A and B (1 at bits 7-9 and 10-12),
+// 32-bit integer accumulator (2 at bits 4-5), both K-major, N >> 3 at bits
+// 17-22, M >> 4 at bits 24-28.
+__device__ __forceinline__ uint32_t idesc_i8(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_i8(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on `bar` (CG 2: on the barrier at that offset of the CTAs in `ctas`)
+// once every MMA issued so far is done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar, uint16_t ctas = 3) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(ctas)
+        : "memory");
+  else
+    tc_commit(bar);
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
+                 : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
+                 : "memory");
+}
+
+// 16 consecutive 32-bit columns of this warp's 32 tensor-memory lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, int (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__host__ __device__ inline uint32_t stage_bytes(int cg, int nt) {
+  return kTileA + (uint32_t)(nt / cg) * kChunk;
+}
+
+// Columns of tensor memory: two accumulators, a power of two from 32.
+__host__ __device__ inline uint32_t tmem_cols(int nt) {
+  uint32_t c = 32;
+  while (c < 2u * nt) c *= 2;
+  return c;
+}
+
+// CG = 2: a cluster of two CTAs works on a tile of 256 output channels (128 in
+// each CTA's tensor memory) and nt tokens, each CTA staging its own 128 rows of
+// W and half of the tokens; the even CTA (leader) issues the MMAs of both.
+// CG = 1: a tile of 128 channels per CTA, or per cluster of `splits` CTAs that
+// share the chunks of the tile and add their integer partial sums through
+// distributed shared memory.
+// Roles meet at mbarriers only: copies fill a ring of stages (full / empty), the
+// MMAs fill one of two accumulators (accfull / accempty), the epilogue warps
+// read the other out.
+template <int CG, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_int8_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                const Int8GemmArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], accfull[2], accempty[2], fin;
+  __shared__ uint32_t tmem_slot;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = CG == 2 || a.splits > 1 ? cluster_rank() : 0u;
+  const int S = a.stages;
+  const uint32_t stage = stage_bytes(CG, a.nt), cols = tmem_cols(a.nt);
+  // tiles of this CTA (pair, cluster): first, first + step, ...
+  const int per = CG == 2 ? 2 : a.splits;
+  const int64_t first = blockIdx.x / per, step = gridDim.x / per;
+  const int c_lo = CG == 2 ? 0 : (int)((int64_t)rank * a.chunks / a.splits);
+  const int c_hi = CG == 2 ? a.chunks : (int)((int64_t)(rank + 1) * a.chunks / a.splits);
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], kEpiWarps * CG);
+    }
+    mbar_init(&fin, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc<CG>(&tmem_slot, cols);
+  tc_fence_before();
+  if (CG == 2)
+    cluster_sync();
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  // every operand and scale may come from the kernel ahead
   pdl_wait();
   pdl_trigger();
-  for (int k0 = 0; k0 < a.d_in; k0 += 64) {
-    for (int e = threadIdx.x; e < kSimpleTile * 16; e += 256) {
-      const int r = e >> 4, k = e & 15;
-      xs[r][k] = t0 + r < a.ntok
-                     ? *reinterpret_cast<const int*>(a.x + (int64_t)(t0 + r) * a.d_in + k0 + 4 * k)
-                     : 0;
-      ws[r][k] = i0 + r < a.d_out
-                     ? *reinterpret_cast<const int*>(a.w + (i0 + r) * a.d_in + k0 + 4 * k)
-                     : 0;
+  int flags = 0;
+
+  if (warp == kCopyWarp) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t u = 0;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int64_t tile = first; tile < a.tiles && ok; tile += step) {
+        const int64_t m = tile / a.tok_tiles;
+        const int row = (int)(m * (kRowsM * CG)) + (CG == 2 ? (int)rank * kRowsM : 0);
+        const int tok = (int)(tile - m * a.tok_tiles) * a.nt + (CG == 2 ? (int)rank * (a.nt / 2) : 0);
+        for (int c = c_lo; c < c_hi; ++c) {
+          if (u > 0 && !mbar_wait_bounded(&empty[s], (u - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          if (CG == 1 || rank == 0) mbar_expect_tx(&full[s], stage * CG);
+          const uint32_t bar = CG == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+          const uint32_t dst = smem_u32(smem) + (uint32_t)s * stage;
+          copy_box<CG>(dst, &map_w, c * kChunk, row, bar);
+          copy_box<CG>(dst + kTileA, &map_x, c * kChunk, tok, bar);
+          ++issued;
+          if (++s == S) {
+            s = 0;
+            ++u;
+          }
+        }
+      }
+      // nothing in flight at exit: the last use of each stage has been consumed
+      // (which also means that a pair's arrivals on these barriers have landed)
+      const int64_t last = issued > S ? issued - S : 0;
+      for (int64_t j = last; j < issued && ok; ++j)
+        ok = mbar_wait_bounded(&empty[j % S], (uint32_t)(j / S) & 1u);
+      if (!ok) {  // given up: the copies at least have to land (a pair's leader waits for both)
+        flags |= QAMW_STATUS_TIMEOUT;
+        if (CG == 1 || rank == 0)
+          for (int64_t j = last; j < issued; ++j)
+            if (!mbar_wait_bounded(&full[j % S], (uint32_t)(j / S) & 1u)) break;
+      }
     }
-    __syncthreads();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && (CG == 1 || rank == 0)) {
+      const uint32_t idesc = idesc_i8(kRowsM * CG, a.nt);
+      int s = 0, n = 0;
+      uint32_t u = 0;
+      bool ok = true;
+      for (int64_t tile = first; tile < a.tiles && ok; tile += step, ++n) {
+        const int b = n & 1;
+        if (n >= 2 && !mbar_wait_bounded(&accempty[b], (uint32_t)((n >> 1) - 1) & 1u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(b * a.nt);
+        for (int c = c_lo; c < c_hi; ++c) {
+          if (!mbar_wait_bounded(&full[s], u & 1u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem) + (uint32_t)s * stage;
+          const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kTileA);
+          const int steps = c == a.chunks - 1 ? a.tail : kChunk / 32;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
+          for (int k = 0; k < kChunk / 32; ++k)  // 32 bytes of a row per MMA
+            if (k < steps) mma_i8<CG>(d, da + 2u * k, db + 2u * k, idesc, (c > c_lo || k > 0) ? 1u : 0u);
+          commit<CG>(&empty[s]);
+          if (++s == S) {
+            s = 0;
+            ++u;
+          }
+        }
+        if (ok) commit<CG>(&accfull[b]);
+      }
+      if (!ok) flags |= QAMW_STATUS_TIMEOUT;
+      // every MMA is done before the tensor memory and the stages are given up
+      commit<CG>(&fin, 1);
+      if (!mbar_wait_bounded(&fin, 0)) flags |= QAMW_STATUS_TIMEOUT;
+    }
+  } else if (CG == 2 || a.splits == 1) {
+    T* y = reinterpret_cast<T*>(a.y);
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
+    int n = 0;
+    for (int64_t tile = first; tile < a.tiles; tile += step, ++n) {
+      const int b = n & 1;
+      const bool ok = mbar_wait_bounded(&accfull[b], (uint32_t)(n >> 1) & 1u);
+      if (__any_sync(0xffffffffu, !ok)) {
+        flags |= QAMW_STATUS_TIMEOUT;
+        break;
+      }
+      tc_fence_after();
+      const int64_t m = tile / a.tok_tiles;
+      const int64_t i = m * (kRowsM * CG) + (CG == 2 ? (int64_t)rank * kRowsM : 0) + 32 * warp + lane;
+      const int t0 = (int)(tile - m * a.tok_tiles) * a.nt;
+      const int nt = min(a.nt, a.ntok - t0);
+      const bool mine = i < a.d_out;
+      const float wi = mine ? __ldg(a.ws + i) : 0.f;
+      for (int c = 0; c < nt; c += 16) {
+        int v[16];
+        tmem_ld16(lane_base + (uint32_t)(b * a.nt + c), v);
+        const int64_t at = (int64_t)(t0 + c) * a.d_out + i;
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int e = 0; e < 16; ++e)
+          if (mine && c + e < nt)
+            put(y, at + (int64_t)e * a.d_out, __fmul_rn((float)v[e], __fmul_rn(__ldg(a.xs + t0 + c + e), wi)));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          mbar_arrive_cluster(cluster_addr(smem_u32(&accempty[b]), 0));
+        else
+          mbar_arrive(&accempty[b]);
+      }
+    }
+  } else {
+    // the CTA's partial sums into its own shared memory (the stages are free:
+    // every MMA that reads them is done), [token][channel]
+    int* part = reinterpret_cast<int*>(smem);
+    const bool ok = mbar_wait_bounded(&accfull[0], 0);
+    if (__any_sync(0xffffffffu, !ok)) flags |= QAMW_STATUS_TIMEOUT;
+    tc_fence_after();
+    for (int c = 0; c < a.nt; c += 16) {
+      int v[16];
+      tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)c, v);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          acc[r][s] = __dp4a(xs[tt + 16 * r][k], ws[ti + 16 * s][k], acc[r][s]);
-    __syncthreads();
+      for (int e = 0; e < 16; ++e) part[(c + e) * kRowsM + tid] = v[e];
+    }
   }
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int t = t0 + tt + 16 * r;
-      const int64_t i = i0 + ti + 16 * s;
-      if (t < a.ntok && i < a.d_out)
-        put(reinterpret_cast<T*>(a.y), (int64_t)t * a.d_out + i,
-            __fmul_rn((float)acc[r][s], __fmul_rn(a.xs[t], a.ws[i])));
+  tc_fence_before();
+  if (CG == 1 && a.splits > 1) {
+    __syncwarp();
+    cluster_sync();
+    // CTA r adds up and writes tokens r, r + splits, ...
+    if (warp < kEpiWarps) {
+      T* y = reinterpret_cast<T*>(a.y);
+      const int64_t m = first / a.tok_tiles;
+      const int64_t i = m * kRowsM + tid;
+      const int t0 = (int)(first - m * a.tok_tiles) * a.nt;
+      const int nt = min(a.nt, a.ntok - t0);
+      const uint32_t base = smem_u32(smem) + 4u * tid;
+      if (i < a.d_out) {
+        const float wi = __ldg(a.ws + i);
+        for (int c = (int)rank; c < nt; c += a.splits) {
+          int v = 0;
+          for (int r = 0; r < a.splits; ++r)
+            v += lds_cluster(cluster_addr(base + 4u * kRowsM * c, (uint32_t)r));
+          put(y, (int64_t)(t0 + c) * a.d_out + i, __fmul_rn((float)v, __fmul_rn(__ldg(a.xs + t0 + c), wi)));
+        }
+      }
     }
+  }
+  __syncwarp();
+  if (CG == 2 || a.splits > 1)
+    cluster_sync();  // no CTA leaves while another reads its memory or signals its barriers
+  else
+    __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_free<CG>(tmem, cols);
+  }
+  raise_flag(a.status, flags);
+}
+
+// 8-bit matrix [rows][d_in] for boxes of 128 bytes x `box` rows, swizzled.
+bool encode_map(CUtensorMap* map, const int8_t* p, int64_t rows, int d_in, int box) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)d_in, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d_in};
+  const cuuint32_t boxes[2] = {kChunk, (cuuint32_t)box};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides, boxes,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Int8Plan {
+  int cg, nt, splits, stages;
+};
+
+Int8Plan plan_int8(int ntok, int d_out, int d_in) {
+  Int8Plan p;
+  const int chunks = (d_in + kChunk - 1) / kChunk;
+  p.splits = 1;
+  if (ntok <= 128) {
+    p.cg = 1;
+    p.nt = (ntok + 15) / 16 * 16;
+    const int tiles = (d_out + kRowsM - 1) / kRowsM;
+    while (p.splits < 8 && tiles * p.splits * 2 <= sm_count() && chunks >= p.splits * 4) p.splits *= 2;
+  } else {
+    p.cg = 2;
+    p.nt = 256;
+  }
+  p.stages = (int)std::min<uint32_t>(kMaxStages, 222u * 1024u / stage_bytes(p.cg, p.nt));
+  return p;
+}
+
+template <int CG, typename T>
+cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap& mx,
+                     const Int8GemmArgs& a, cudaStream_t stream) {
+  // at least 116 KB, so that no two CTAs that own tensor memory share an SM
+  const size_t smem = std::max<size_t>((size_t)p.stages * stage_bytes(p.cg, p.nt) + 1024, 116 * 1024);
+  auto fn = &k_int8_gemm<CG, T>;
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(fn), smem);
+  if (err != cudaSuccess) return err;
+  const int per = CG == 2 ? 2 : p.splits;
+  const int64_t most = p.splits > 1 ? a.tiles : std::max(1, sm_count() / per);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(a.tiles, most) * per));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)per;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = per > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fn, mw, mx, a);
 }
 
 }  // namespace
@@ -71,13 +459,29 @@ __global__ void __launch_bounds__(256) k_int8_gemm(const Int8GemmArgs a) {
 cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
                              int32_t* d_status, cudaStream_t stream) {
-  (void)d_status;
-  Int8GemmArgs a = {d_x, d_x_scale, d_w, d_w_scale, d_y, ntok, d_out, d_in};
-  const dim3 grid((unsigned)((d_out + kSimpleTile - 1) / kSimpleTile),
-                  (unsigned)((ntok + kSimpleTile - 1) / kSimpleTile));
-  return dtype == QAMW_DTYPE_F32
-             ? launch_pdl(k_int8_gemm<float>, grid, dim3(256), 0, stream, a)
-             : launch_pdl(k_int8_gemm<__nv_bfloat16>, grid, dim3(256), 0, stream, a);
+  const Int8Plan p = plan_int8(ntok, d_out, d_in);
+  CUtensorMap mw, mx;
+  if (!encode_map(&mw, d_w, d_out, d_in, kRowsM) || !encode_map(&mx, d_x, ntok, d_in, p.nt / p.cg))
+    return cudaErrorInvalidValue;
+  Int8GemmArgs a = {};
+  a.xs = d_x_scale;
+  a.ws = d_w_scale;
+  a.y = d_y;
+  a.status = d_status;
+  a.ntok = ntok;
+  a.d_out = d_out;
+  a.chunks = (d_in + kChunk - 1) / kChunk;
+  a.tail = (d_in - (a.chunks - 1) * kChunk) / 32;
+  a.nt = p.nt;
+  a.tok_tiles = (ntok + p.nt - 1) / p.nt;
+  a.tiles = (int64_t)((d_out + kRowsM * p.cg - 1) / (kRowsM * p.cg)) * a.tok_tiles;
+  a.stages = p.stages;
+  a.splits = p.splits;
+  if (dtype == QAMW_DTYPE_F32)
+    return p.cg == 2 ? run_gemm<2, float>(p, mw, mx, a, stream)
+                     : run_gemm<1, float>(p, mw, mx, a, stream);
+  return p.cg == 2 ? run_gemm<2, __nv_bfloat16>(p, mw, mx, a, stream)
+                   : run_gemm<1, __nv_bfloat16>(p, mw, mx, a, stream);
 }
 
 }  // namespace qamw
