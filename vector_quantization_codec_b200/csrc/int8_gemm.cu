@@ -40,12 +40,22 @@ struct Int8GemmArgs {
   int nt;          // tokens per tile
   int tok_tiles;
   int stages;
+  int boxes;       // chunks per stage
   int splits;      // CTAs (a cluster) that share a tile's chunks; 1: persistent over tiles
 };
 
 __device__ __forceinline__ void put(float* y, int64_t at, float v) { y[at] = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* y, int64_t at, float v) {
   y[at] = __float2bfloat16_rn(v);
+}
+
+// True in one lane of a converged warp.  The compiler knows that one thread
+// runs what this guards and keeps its operands in uniform registers; behind
+// `lane == 0` four MMAs took 367 cycles to issue, more than they ran.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
 }
 
 // Address of this CTA's shared address `addr` in CTA `rank` of the cluster.
@@ -62,9 +72,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ int lds_cluster(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
+__device__ __forceinline__ int4 lds_cluster(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
@@ -167,7 +179,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, int (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__host__ __device__ inline uint32_t stage_bytes(int cg, int nt) {
+// One 128-byte chunk of a CTA's rows and tokens.
+__host__ __device__ inline uint32_t box_bytes(int cg, int nt) {
   return kTileA + (uint32_t)(nt / cg) * kChunk;
 }
 
@@ -176,6 +189,54 @@ __host__ __device__ inline uint32_t tmem_cols(int nt) {
   uint32_t c = 32;
   while (c < 2u * nt) c *= 2;
   return c;
+}
+
+// Sum of the S partial tiles [token][128 channels] of a cluster: CTA `rank`
+// adds up and writes tokens rank, rank + S, ..., a warp one token at a time, a
+// lane four channels; the loads of kAhead tokens from all S CTAs are in flight
+// together (one distributed shared-memory latency instead of one per token).
+template <int S, typename T>
+__device__ __forceinline__ void add_partials(const Int8GemmArgs& a, int64_t tile, uint32_t rank,
+                                             uint32_t part, int warp, int lane) {
+  constexpr int kAhead = 8 / S > 2 ? 8 / S : 2;
+  T* y = reinterpret_cast<T*>(a.y);
+  const int64_t m = tile / a.tok_tiles;
+  const int64_t i = m * kRowsM + 4 * lane;
+  const int t0 = (int)(tile - m * a.tok_tiles) * a.nt;
+  const int nt = min(a.nt, a.ntok - t0);
+  float w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = i + e < a.d_out ? __ldg(a.ws + i + e) : 0.f;
+  uint32_t from[S];
+#pragma unroll
+  for (int r = 0; r < S; ++r) from[r] = cluster_addr(part + 16u * lane, (uint32_t)r);
+  for (int c0 = (int)rank + S * warp; c0 < nt; c0 += S * kEpiWarps * kAhead) {
+    int4 v[kAhead][S];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int c = min(c0 + j * S * kEpiWarps, a.nt - 1);
+#pragma unroll
+      for (int r = 0; r < S; ++r) v[j][r] = lds_cluster(from[r] + 4u * kRowsM * (uint32_t)c);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int c = c0 + j * S * kEpiWarps;
+      if (c >= nt) break;
+      int sum[4] = {};
+#pragma unroll
+      for (int r = 0; r < S; ++r) {
+        sum[0] += v[j][r].x;
+        sum[1] += v[j][r].y;
+        sum[2] += v[j][r].z;
+        sum[3] += v[j][r].w;
+      }
+      const float xs = __ldg(a.xs + t0 + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < a.d_out)
+          put(y, (int64_t)(t0 + c) * a.d_out + i + e, __fmul_rn((float)sum[e], __fmul_rn(xs, w[e])));
+    }
+  }
 }
 
 // CG = 2: a cluster of two CTAs works on a tile of 256 output channels (128 in
@@ -194,11 +255,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], accfull[2], accempty[2], fin;
+  __shared__ __align__(16) float xs_tile[kEpiWarps][256];
   __shared__ uint32_t tmem_slot;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = CG == 2 || a.splits > 1 ? cluster_rank() : 0u;
   const int S = a.stages;
-  const uint32_t stage = stage_bytes(CG, a.nt), cols = tmem_cols(a.nt);
+  const uint32_t box = box_bytes(CG, a.nt), stage = box * a.boxes, cols = tmem_cols(a.nt);
   // tiles of this CTA (pair, cluster): first, first + step, ...
   const int per = CG == 2 ? 2 : a.splits;
   const int64_t first = blockIdx.x / per, step = gridDim.x / per;
@@ -231,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int flags = 0;
 
   if (warp == kCopyWarp) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t u = 0;
       int64_t issued = 0;
@@ -240,16 +302,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t m = tile / a.tok_tiles;
         const int row = (int)(m * (kRowsM * CG)) + (CG == 2 ? (int)rank * kRowsM : 0);
         const int tok = (int)(tile - m * a.tok_tiles) * a.nt + (CG == 2 ? (int)rank * (a.nt / 2) : 0);
-        for (int c = c_lo; c < c_hi; ++c) {
+        for (int c = c_lo; c < c_hi; c += a.boxes) {
+          const int nb = min(a.boxes, c_hi - c);
           if (u > 0 && !mbar_wait_bounded(&empty[s], (u - 1) & 1u)) {
             ok = false;
             break;
           }
-          if (CG == 1 || rank == 0) mbar_expect_tx(&full[s], stage * CG);
+          if (CG == 1 || rank == 0) mbar_expect_tx(&full[s], box * CG * nb);
           const uint32_t bar = CG == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-          const uint32_t dst = smem_u32(smem) + (uint32_t)s * stage;
-          copy_box<CG>(dst, &map_w, c * kChunk, row, bar);
-          copy_box<CG>(dst + kTileA, &map_x, c * kChunk, tok, bar);
+          uint32_t dst = smem_u32(smem) + (uint32_t)s * stage;
+          for (int j = 0; j < nb; ++j, dst += box) {
+            copy_box<CG>(dst, &map_w, (c + j) * kChunk, row, bar);
+            copy_box<CG>(dst + kTileA, &map_x, (c + j) * kChunk, tok, bar);
+          }
           ++issued;
           if (++s == S) {
             s = 0;
@@ -270,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && (CG == 1 || rank == 0)) {
+    if ((CG == 1 || rank == 0) && elect_one()) {
       const uint32_t idesc = idesc_i8(kRowsM * CG, a.nt);
       int s = 0, n = 0;
       uint32_t u = 0;
@@ -283,18 +348,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(b * a.nt);
-        for (int c = c_lo; c < c_hi; ++c) {
+        for (int c = c_lo; c < c_hi; c += a.boxes) {
+          const int nb = min(a.boxes, c_hi - c);
           if (!mbar_wait_bounded(&full[s], u & 1u)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem) + (uint32_t)s * stage;
-          const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kTileA);
-          const int steps = c == a.chunks - 1 ? a.tail : kChunk / 32;
+          uint32_t sa = smem_u32(smem) + (uint32_t)s * stage;
+          for (int j = 0; j < nb; ++j, sa += box) {
+            const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kTileA);
+            const int steps = c + j == a.chunks - 1 ? a.tail : kChunk / 32;
 #pragma unroll
-          for (int k = 0; k < kChunk / 32; ++k)  // 32 bytes of a row per MMA
-            if (k < steps) mma_i8<CG>(d, da + 2u * k, db + 2u * k, idesc, (c > c_lo || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kChunk / 32; ++k)  // 32 bytes of a row per MMA
+              if (k < steps)
+                mma_i8<CG>(d, da + 2u * k, db + 2u * k, idesc, (c + j > c_lo || k > 0) ? 1u : 0u);
+          }
           commit<CG>(&empty[s]);
           if (++s == S) {
             s = 0;
@@ -311,29 +379,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (CG == 2 || a.splits == 1) {
     T* y = reinterpret_cast<T*>(a.y);
     const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
+    float* xs = xs_tile[warp];
     int n = 0;
     for (int64_t tile = first; tile < a.tiles; tile += step, ++n) {
       const int b = n & 1;
-      const bool ok = mbar_wait_bounded(&accfull[b], (uint32_t)(n >> 1) & 1u);
-      if (__any_sync(0xffffffffu, !ok)) {
-        flags |= QAMW_STATUS_TIMEOUT;
-        break;
-      }
-      tc_fence_after();
       const int64_t m = tile / a.tok_tiles;
       const int64_t i = m * (kRowsM * CG) + (CG == 2 ? (int64_t)rank * kRowsM : 0) + 32 * warp + lane;
       const int t0 = (int)(tile - m * a.tok_tiles) * a.nt;
       const int nt = min(a.nt, a.ntok - t0);
       const bool mine = i < a.d_out;
       const float wi = mine ? __ldg(a.ws + i) : 0.f;
-      for (int c = 0; c < nt; c += 16) {
+      for (int c = lane; c < a.nt; c += 32) xs[c] = c < nt ? __ldg(a.xs + t0 + c) : 0.f;
+      // one lane polls: 32 pollers a warp would slow the other roles' waits
+      const bool ok = lane != 0 || mbar_wait_bounded(&accfull[b], (uint32_t)(n >> 1) & 1u);
+      if (__any_sync(0xffffffffu, !ok)) {
+        flags |= QAMW_STATUS_TIMEOUT;
+        break;
+      }
+      tc_fence_after();
+      T* out = y + (int64_t)t0 * a.d_out + i;
+      const int64_t pitch = a.d_out;
+      for (int c = 0; c < nt; c += 16, out += 16 * pitch) {
         int v[16];
         tmem_ld16(lane_base + (uint32_t)(b * a.nt + c), v);
-        const int64_t at = (int64_t)(t0 + c) * a.d_out + i;
+        float f[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (mine && c + e < nt)
-            put(y, at + (int64_t)e * a.d_out, __fmul_rn((float)v[e], __fmul_rn(__ldg(a.xs + t0 + c + e), wi)));
+        for (int e = 0; e < 16; ++e) f[e] = __fmul_rn((float)v[e], __fmul_rn(xs[c + e], wi));
+        if (mine) {
+          if (c + 16 <= nt) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) put(out, e * pitch, f[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c + e < nt) put(out, e * pitch, f[e]);
+          }
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -348,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the CTA's partial sums into its own shared memory (the stages are free:
     // every MMA that reads them is done), [token][channel]
     int* part = reinterpret_cast<int*>(smem);
-    const bool ok = mbar_wait_bounded(&accfull[0], 0);
+    const bool ok = lane != 0 || mbar_wait_bounded(&accfull[0], 0);
     if (__any_sync(0xffffffffu, !ok)) flags |= QAMW_STATUS_TIMEOUT;
     tc_fence_after();
     for (int c = 0; c < a.nt; c += 16) {
@@ -362,23 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (CG == 1 && a.splits > 1) {
     __syncwarp();
     cluster_sync();
-    // CTA r adds up and writes tokens r, r + splits, ...
     if (warp < kEpiWarps) {
-      T* y = reinterpret_cast<T*>(a.y);
-      const int64_t m = first / a.tok_tiles;
-      const int64_t i = m * kRowsM + tid;
-      const int t0 = (int)(first - m * a.tok_tiles) * a.nt;
-      const int nt = min(a.nt, a.ntok - t0);
-      const uint32_t base = smem_u32(smem) + 4u * tid;
-      if (i < a.d_out) {
-        const float wi = __ldg(a.ws + i);
-        for (int c = (int)rank; c < nt; c += a.splits) {
-          int v = 0;
-          for (int r = 0; r < a.splits; ++r)
-            v += lds_cluster(cluster_addr(base + 4u * kRowsM * c, (uint32_t)r));
-          put(y, (int64_t)(t0 + c) * a.d_out + i, __fmul_rn((float)v, __fmul_rn(__ldg(a.xs + t0 + c), wi)));
-        }
-      }
+      if (a.splits == 2)
+        add_partials<2, T>(a, first, rank, smem_u32(smem), warp, lane);
+      else if (a.splits == 4)
+        add_partials<4, T>(a, first, rank, smem_u32(smem), warp, lane);
+      else
+        add_partials<8, T>(a, first, rank, smem_u32(smem), warp, lane);
     }
   }
   __syncwarp();
@@ -407,7 +478,7 @@ bool encode_map(CUtensorMap* map, const int8_t* p, int64_t rows, int d_in, int b
 }
 
 struct Int8Plan {
-  int cg, nt, splits, stages;
+  int cg, nt, splits, boxes, stages;
 };
 
 Int8Plan plan_int8(int ntok, int d_out, int d_in) {
@@ -423,7 +494,12 @@ Int8Plan plan_int8(int ntok, int d_out, int d_in) {
     p.cg = 2;
     p.nt = 256;
   }
-  p.stages = (int)std::min<uint32_t>(kMaxStages, 222u * 1024u / stage_bytes(p.cg, p.nt));
+  // the wait for a stage and its commit cost the MMA thread about 240 cycles:
+  // several chunks per stage, as long as three stages fit
+  constexpr uint32_t kRing = 218u * 1024u;
+  p.boxes = 4;
+  while (p.boxes > 1 && kRing / (box_bytes(p.cg, p.nt) * p.boxes) < 3) p.boxes /= 2;
+  p.stages = (int)std::min<uint32_t>(kMaxStages, kRing / (box_bytes(p.cg, p.nt) * p.boxes));
   return p;
 }
 
@@ -431,7 +507,7 @@ template <int CG, typename T>
 cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap& mx,
                      const Int8GemmArgs& a, cudaStream_t stream) {
   // at least 116 KB, so that no two CTAs that own tensor memory share an SM
-  const size_t smem = std::max<size_t>((size_t)p.stages * stage_bytes(p.cg, p.nt) + 1024, 116 * 1024);
+  const size_t smem = std::max<size_t>((size_t)p.stages * p.boxes * box_bytes(p.cg, p.nt) + 1024, 116 * 1024);
   auto fn = &k_int8_gemm<CG, T>;
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(fn), smem);
   if (err != cudaSuccess) return err;
@@ -476,6 +552,7 @@ cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok
   a.tok_tiles = (ntok + p.nt - 1) / p.nt;
   a.tiles = (int64_t)((d_out + kRowsM * p.cg - 1) / (kRowsM * p.cg)) * a.tok_tiles;
   a.stages = p.stages;
+  a.boxes = p.boxes;
   a.splits = p.splits;
   if (dtype == QAMW_DTYPE_F32)
     return p.cg == 2 ? run_gemm<2, float>(p, mw, mx, a, stream)
