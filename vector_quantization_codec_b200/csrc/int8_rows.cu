@@ -158,24 +158,64 @@ __device__ __forceinline__ RowRed reduce_row(RowRed r, bool by_warp, RowRed* slo
   return o;
 }
 
-// A row belongs to one warp (by_warp: d <= 1024, a CTA takes a row per warp) or
-// to the whole CTA; its thread t of n holds vectors t, t + n, ... of eight
-// columns.  c_j of those columns is formed once for all rows of the thread.
-template <typename T, int VEC, bool NORM, bool RES>
-__global__ void __launch_bounds__(1024, 1) k_int8_rows(const Int8RowsArgs a, bool by_warp) {
+// Rows of c in shared memory: eight columns as two float4, 16 bytes apart by
+// half the row, so that a warp's 16-byte loads are consecutive.
+__device__ __forceinline__ void put_factors(float4* tab, int nvec, int v, const float (&c)[8]) {
+  tab[v] = make_float4(c[0], c[1], c[2], c[3]);
+  tab[nvec + v] = make_float4(c[4], c[5], c[6], c[7]);
+}
+__device__ __forceinline__ void get_factors(const float4* tab, int nvec, int v, float (&c)[8]) {
+  const float4 a = tab[v], b = tab[nvec + v];
+  c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+  c[4] = b.x, c[5] = b.y, c[6] = b.z, c[7] = b.w;
+}
+
+// Four rounded values as the bytes of a word.  x + 1.5 2^23 rounds x to a whole
+// number (ties to even) whose low byte is the low byte of the sum's pattern: an
+// addition in place of a conversion, which has a quarter of its rate.
+__device__ __forceinline__ uint32_t pack_rounded(float a, float b, float c, float d) {
+  constexpr float kMagic = 12582912.f;
+  const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(a, kMagic)),
+                                  __float_as_uint(__fadd_rn(b, kMagic)), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(__fadd_rn(c, kMagic)),
+                                  __float_as_uint(__fadd_rn(d, kMagic)), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// How a row is shared out (MODE) and where its thread keeps c_j:
+//   kWarpRow  a warp per row, eight rows a CTA (d <= 1024); c in registers;
+//   kWideRow  a CTA per row, one vector of eight columns a thread; c in
+//             registers: the shortest chain for a few rows;
+//   kDeepRow  a CTA per row, VEC vectors a thread; c in shared memory, so that
+//             the registers allow about a thousand threads per SM, each with
+//             VEC loads per input in flight.
+enum { kWarpRow, kWideRow, kDeepRow };
+
+template <typename T, int MODE, int VEC, bool NORM, bool RES>
+__global__ void __launch_bounds__(MODE == kWarpRow ? 256 : 1024, 1)
+    k_int8_rows(const Int8RowsArgs a) {
   __shared__ RowRed slots[2][32];
-  const int n = by_warp ? 32 : blockDim.x;
-  const int t = by_warp ? (threadIdx.x & 31) : threadIdx.x;
+  extern __shared__ __align__(16) float4 c_tab[];
+  constexpr bool kByWarp = MODE == kWarpRow;
+  const int n = kByWarp ? 32 : blockDim.x;
+  const int t = kByWarp ? (threadIdx.x & 31) : threadIdx.x;
   const int nvec = a.d / 8;
-  const int64_t groups = by_warp ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
+  const int64_t groups = kByWarp ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
   const int64_t first =
-      by_warp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+      kByWarp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   pdl_wait();
   pdl_trigger();
-  float c[VEC][8];
+  float c[MODE == kDeepRow ? 1 : VEC][8];
+  if constexpr (MODE == kDeepRow) {
+    for (int v = t; v < nvec; v += n) {  // each thread reads back what it wrote
+      factors<T, NORM>(a, v, c[0]);
+      put_factors(c_tab, nvec, v, c[0]);
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i)
-    if (t + i * n < nvec) factors<T, NORM>(a, t + i * n, c[i]);
+    for (int i = 0; i < VEC; ++i)
+      if (t + i * n < nvec) factors<T, NORM>(a, t + i * n, c[i]);
+  }
   int flags = 0, parity = 0;
   for (int64_t row = first; row < a.rows; row += groups) {
     const int64_t base = row * nvec;
@@ -183,10 +223,8 @@ __global__ void __launch_bounds__(1024, 1) k_int8_rows(const Int8RowsArgs a, boo
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const int v = t + i * n;
-      if (v < nvec)
-        h[i].load(a.x, base + v);
-      else
-        h[i].zero();
+      h[i].zero();
+      if (v < nvec) h[i].load(a.x, base + v);
     }
     if constexpr (RES) {
 #pragma unroll
@@ -196,8 +234,12 @@ __global__ void __launch_bounds__(1024, 1) k_int8_rows(const Int8RowsArgs a, boo
           Raw8<T> r;
           r.load(a.res, base + v);
           h[i].add(r);
-          h[i].store(a.sum, base + v);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const int v = t + i * n;
+        if (v < nvec) h[i].store(a.sum, base + v);
       }
     }
     RowRed r;
@@ -206,14 +248,15 @@ __global__ void __launch_bounds__(1024, 1) k_int8_rows(const Int8RowsArgs a, boo
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       if (t + i * n < nvec) {
+        if constexpr (MODE == kDeepRow) get_factors(c_tab, nvec, t + i * n, c[0]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float f = h[i].get(e);
           if constexpr (NORM) r.sum = fmaf(f, f, r.sum);
-          r.top = max(r.top, __float_as_uint(fabsf(__fmul_rn(f, c[i][e]))));
+          r.top = max(r.top, __float_as_uint(fabsf(__fmul_rn(f, c[MODE == kDeepRow ? 0 : i][e]))));
         }
       }
-    r = reduce_row<NORM>(r, by_warp, slots[parity]);
+    r = reduce_row<NORM>(r, kByWarp, slots[parity]);
     parity ^= 1;
     const float top = __uint_as_float(r.top);
     const bool finite = r.top < kInfBits, some = finite && top >= kRowTiny;
@@ -221,21 +264,19 @@ __global__ void __launch_bounds__(1024, 1) k_int8_rows(const Int8RowsArgs a, boo
     float scale = some ? __fdiv_rn(top, kInt8Max) : 0.f;
     if constexpr (NORM) {
       if (some && r.sum > FLT_MAX) {
-        // the squares overflow (|h| beyond 2^56): again with h 2^-70, whose
+        // the squares overflow (|h| beyond about 2^56): again with h 2^-70, whose
         // squares fit; what underflows there is far below the row's largest
         RowRed w;
         w.sum = 0.f;
         w.top = 0u;
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-          if (t + i * n < nvec) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float f = h[i].get(e) * 8.470329472543003e-22f;
-              w.sum = fmaf(f, f, w.sum);
-            }
+          for (int e = 0; e < 8; ++e) {
+            const float f = h[i].get(e) * 8.470329472543003e-22f;
+            w.sum = fmaf(f, f, w.sum);
           }
-        w = reduce_row<NORM>(w, by_warp, slots[parity]);
+        w = reduce_row<NORM>(w, kByWarp, slots[parity]);
         parity ^= 1;
         scale = scale * 8.470329472543003e-22f * (1.f / sqrtf(w.sum / (float)a.d));
       } else {
@@ -250,52 +291,46 @@ __global__ void __launch_bounds__(1024, 1) k_int8_rows(const Int8RowsArgs a, boo
     for (int i = 0; i < VEC; ++i) {
       const int v = t + i * n;
       if (v < nvec) {
-        uint32_t w[2];
+        if constexpr (MODE == kDeepRow) get_factors(c_tab, nvec, v, c[0]);
+        float f[8];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          int k[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            k[e] = some ? __float2int_rn(__fmul_rn(__fmul_rn(h[i].get(4 * p + e), c[i][4 * p + e]), inv))
-                        : 0;
-          w[p] = (uint32_t)(k[0] & 0xff) | ((uint32_t)(k[1] & 0xff) << 8) |
-                 ((uint32_t)(k[2] & 0xff) << 16) | ((uint32_t)k[3] << 24);
-        }
-        reinterpret_cast<uint2*>(a.q)[base + v] = make_uint2(w[0], w[1]);
+        for (int e = 0; e < 8; ++e)
+          f[e] = __fmul_rn(__fmul_rn(h[i].get(e), c[MODE == kDeepRow ? 0 : i][e]), inv);
+        uint2 w = make_uint2(pack_rounded(f[0], f[1], f[2], f[3]), pack_rounded(f[4], f[5], f[6], f[7]));
+        if (!some) w = make_uint2(0u, 0u);
+        reinterpret_cast<uint2*>(a.q)[base + v] = w;
       }
     }
   }
   raise_flag(a.status, flags);
 }
 
-template <typename T, int VEC, bool NORM, bool RES>
-cudaError_t run_rows(const Int8RowsArgs& a, int threads, bool by_warp, cudaStream_t stream) {
-  const void* fn = reinterpret_cast<const void*>(&k_int8_rows<T, VEC, NORM, RES>);
-  const int64_t per = by_warp ? threads / 32 : 1;
-  const int grid = persistent_grid(fn, threads, 0, (a.rows + per - 1) / per);
-  return launch_pdl(k_int8_rows<T, VEC, NORM, RES>, dim3(grid), dim3(threads), 0, stream, a,
-                    by_warp);
+template <typename T, int MODE, int VEC, bool NORM, bool RES>
+cudaError_t run_rows(const Int8RowsArgs& a, int threads, cudaStream_t stream) {
+  auto fn = &k_int8_rows<T, MODE, VEC, NORM, RES>;
+  const size_t smem = MODE == kDeepRow ? (size_t)a.d * sizeof(float) : 0;
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(fn), smem);
+  if (err != cudaSuccess) return err;
+  const int64_t per = MODE == kWarpRow ? threads / 32 : 1;
+  const int grid =
+      persistent_grid(reinterpret_cast<const void*>(fn), threads, smem, (a.rows + per - 1) / per);
+  return launch_pdl(fn, dim3(grid), dim3(threads), smem, stream, a);
 }
 
 template <typename T, bool NORM, bool RES>
 cudaError_t run_rows_any(const Int8RowsArgs& a, cudaStream_t stream) {
   const int nvec = a.d / 8;
-  const bool by_warp = a.d <= 1024;
-  int vec, threads;
-  if (by_warp) {
-    vec = (nvec + 31) / 32;
-    threads = (int)std::min<int64_t>(8, a.rows) * 32;
-  } else {
-    vec = std::max(1, (nvec + 1023) / 1024);
-    threads = ((nvec + vec - 1) / vec + 31) / 32 * 32;
+  if (a.d <= 1024) {
+    const int threads = (int)std::min<int64_t>(8, a.rows) * 32;
+    switch ((nvec + 31) / 32) {
+      case 1: return run_rows<T, kWarpRow, 1, NORM, RES>(a, threads, stream);
+      case 2: return run_rows<T, kWarpRow, 2, NORM, RES>(a, threads, stream);
+      default: return run_rows<T, kWarpRow, 4, NORM, RES>(a, threads, stream);
+    }
   }
-  switch (vec) {
-    case 1: return run_rows<T, 1, NORM, RES>(a, threads, by_warp, stream);
-    case 2: return run_rows<T, 2, NORM, RES>(a, threads, by_warp, stream);
-    case 3: return run_rows<T, 3, NORM, RES>(a, threads, by_warp, stream);
-    case 4: return run_rows<T, 4, NORM, RES>(a, threads, by_warp, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  if (a.rows <= 2 * sm_count() && nvec <= 1024)
+    return run_rows<T, kWideRow, 1, NORM, RES>(a, (nvec + 31) / 32 * 32, stream);
+  return run_rows<T, kDeepRow, 4, NORM, RES>(a, ((nvec + 3) / 4 + 31) / 32 * 32, stream);
 }
 
 }  // namespace
