@@ -499,11 +499,12 @@ def qamw_decode_gemv_noalloc(m: EncodedMatrix, x: torch.Tensor, y: torch.Tensor,
 _DTYPE_CODE = {torch.float32: QAMW_DTYPE_F32, torch.bfloat16: QAMW_DTYPE_BF16}
 
 
-def _dense(name: str, t: torch.Tensor, dtype, shape: tuple, device) -> int:
-    """Device address of a tensor that must be dense, of this type and shape, on `device`."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+def _dense(name: str, t: torch.Tensor, dtype, shape: tuple, index: int) -> int:
+    """Device address of a tensor that must be dense, of this type and shape, on GPU `index`."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != index
+            or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{device}, not {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"cuda:{index}, not {t.dtype} {tuple(t.shape)} on {t.device}"
                          f"{'' if t.is_contiguous() else ' (strided)'}")
     return t.data_ptr()
 
@@ -517,53 +518,52 @@ def _rows_of(name: str, x: torch.Tensor) -> int:
     return code
 
 
-class _On:
-    """Makes `device` current, with `stream` (when given) the current stream, for
-    the allocations and the launch inside; `.handle` is the stream to launch on."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.stack = device, stream, None
-
-    def __enter__(self):
-        if self.stream is None and self.device.index == torch.cuda.current_device():
-            self.handle = torch.cuda.current_stream().cuda_stream
-            return self
-        self.stack = contextlib.ExitStack()
-        self.stack.enter_context(torch.cuda.device(self.device))
-        if self.stream is not None:
-            s = self.stream
-            if not hasattr(s, "cuda_stream"):
-                s = torch.cuda.ExternalStream(int(s), device=self.device)
-            if s.device != self.device:
-                self.stack.close()
-                raise ValueError(f"the stream is on {s.device}, the tensors are on {self.device}")
-            self.stack.enter_context(torch.cuda.stream(s))
-        self.handle = torch.cuda.current_stream().cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        if self.stack is not None:
-            self.stack.close()
+# The current stream's handle without building a Stream object (a few microseconds a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _status_ptr(status: torch.Tensor | None, device):
-    return None if status is None else _dense("status", status, torch.int32, status.shape, device)
+def _enter(index: int, stream):
+    """Makes GPU `index` current and `stream` (when given) its current stream, so that what is
+    allocated next belongs to the stream it is used on; None when that is so already, else the
+    context to close."""
+    if stream is None and torch.cuda.current_device() == index:
+        return None
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(index))
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = (torch.cuda.ExternalStream(int(stream), device=index) if int(stream)
+                      else torch.cuda.default_stream(index))
+        if stream.device.index != index:
+            ctx.close()
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
+
+
+def _status_ptr(status: torch.Tensor | None, index: int):
+    return None if status is None else _dense("status", status, torch.int32, status.shape, index)
 
 
 def _int8_encode(fn: str, what: str, x, chan_scale, q, scale, status, stream):
     code = _rows_of(what, x)
     rows, d = x.shape
-    dev = x.device
-    with _On(dev, stream) as on:
+    dev = x.get_device()
+    ctx = _enter(dev, stream)
+    try:
         if q is None:
-            q = torch.empty((rows, d), dtype=torch.int8, device=dev)
+            q = torch.empty_like(x, dtype=torch.int8)
         if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=dev)
+            scale = x.new_empty(rows, dtype=torch.float32)
         _check(fn, getattr(_lib, fn)(
             x.data_ptr(), code, rows, d,
             None if chan_scale is None else _dense("chan_scale", chan_scale, torch.float16, (d,), dev),
             _dense("q", q, torch.int8, (rows, d), dev),
-            _dense("scale", scale, torch.float32, (rows,), dev), _status_ptr(status, dev), on.handle))
+            _dense("scale", scale, torch.float32, (rows,), dev), _status_ptr(status, dev),
+            _raw_stream(dev)))
+    finally:
+        if ctx is not None:
+            ctx.close()
     return q, scale
 
 
@@ -593,25 +593,29 @@ def qamw_rmsnorm_int8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-5,
     (q, tok_scale) without a residual; sum_out (which h is written to) may be x or residual."""
     code = _rows_of("x", x)
     rows, d = x.shape
-    dev = x.device
+    dev = x.get_device()
     if residual is None and sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    with _On(dev, stream) as on:
+    ctx = _enter(dev, stream)
+    try:
         if residual is not None and sum_out is None:
             sum_out = torch.empty_like(x)
         if q is None:
-            q = torch.empty((rows, d), dtype=torch.int8, device=dev)
+            q = torch.empty_like(x, dtype=torch.int8)
         if tok_scale is None:
-            tok_scale = torch.empty(rows, dtype=torch.float32, device=dev)
+            tok_scale = x.new_empty(rows, dtype=torch.float32)
         _check("qamw_rmsnorm_int8", _lib.qamw_rmsnorm_int8(
             x.data_ptr(),
-            None if residual is None else _dense("residual", residual, x.dtype, x.shape, dev),
-            code, _dense("gain", gain, x.dtype, (d,), dev), float(eps), rows, d,
+            None if residual is None else _dense("residual", residual, x.dtype, (rows, d), dev),
+            code, _dense("gain", gain, x.dtype, (d,), dev), eps, rows, d,
             None if chan_scale is None else _dense("chan_scale", chan_scale, torch.float16, (d,), dev),
-            None if residual is None else _dense("sum_out", sum_out, x.dtype, x.shape, dev),
+            None if residual is None else _dense("sum_out", sum_out, x.dtype, (rows, d), dev),
             _dense("q", q, torch.int8, (rows, d), dev),
             _dense("tok_scale", tok_scale, torch.float32, (rows,), dev),
-            _status_ptr(status, dev), on.handle))
+            _status_ptr(status, dev), _raw_stream(dev)))
+    finally:
+        if ctx is not None:
+            ctx.close()
     return (q, tok_scale) if residual is None else (sum_out, q, tok_scale)
 
 
@@ -624,19 +628,24 @@ def qamw_int8_gemm(xq: torch.Tensor, tok_scale: torch.Tensor, wq: torch.Tensor,
     if xq.dim() != 2 or wq.dim() != 2 or not xq.is_cuda:
         raise ValueError("xq and wq must be int8 [ntok, d_in] and [d_out, d_in] tensors on a GPU")
     ntok, d_in = xq.shape
-    d_out, dev = wq.shape[0], xq.device
+    d_out, dev = wq.shape[0], xq.get_device()
     if y is not None:
         dtype = y.dtype
     code = _DTYPE_CODE.get(dtype)
     if code is None:
         raise ValueError(f"y must be float32 or bfloat16, not {dtype}")
-    with _On(dev, stream) as on:
+    ctx = _enter(dev, stream)
+    try:
         if y is None:
-            y = torch.empty((ntok, d_out), dtype=dtype, device=dev)
+            y = xq.new_empty((ntok, d_out), dtype=dtype)
         _check("qamw_int8_gemm", _lib.qamw_int8_gemm(
             _dense("xq", xq, torch.int8, (ntok, d_in), dev),
             _dense("tok_scale", tok_scale, torch.float32, (ntok,), dev), ntok,
             _dense("wq", wq, torch.int8, (d_out, d_in), dev),
             _dense("row_scale", row_scale, torch.float32, (d_out,), dev), d_out, d_in,
-            _dense("y", y, dtype, (ntok, d_out), dev), code, _status_ptr(status, dev), on.handle))
+            _dense("y", y, dtype, (ntok, d_out), dev), code, _status_ptr(status, dev),
+            _raw_stream(dev)))
+    finally:
+        if ctx is not None:
+            ctx.close()
     return y
