@@ -107,7 +107,32 @@ def test_rmsnorm(d, residual, kind):
         assert out[1][2].item() == 0 and not out[0][2].any()
 
 
-@pytest.mark.parametrize("rows,d", [(1, 4096), (300, 64), (1000, 2048), (2, 32768)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [256, 1024, 1088, 2048, 4096, 5120, 6144, 8192, 11008, 12288, 13824, 16384,
+                               16448, 25600, 32768])
+def test_many_rows(d, kind):
+    """Batches of more rows than the device takes at once, rows of zeros and of other scales among
+    them."""
+    rows, eps = 700, 1e-5
+    x = values(rows, d, kind, d)
+    x *= torch.logspace(-6, 4, rows, device=DEV).to(x.dtype)[:, None]
+    x[[0, 311, rows - 1]] = 0
+    s, sn = chan_scale(d, 4), chan_scale(d, 4).cpu().numpy()
+    gain = (1 + 0.2 * values(1, d, kind, 3)[0].clamp(-3, 3))
+    st = status()
+    q, scale = qamw.qamw_int8_encode_weights(x, s, status=st)
+    check_rows(q, scale, x, ref.factors32(d, sn, None, False), sn, None, False)
+    for res in (None, x.flip(0).contiguous()):
+        out = qamw.qamw_rmsnorm_int8(x, gain, eps, residual=res, chan_scale=s, status=st)
+        h = x
+        if res is not None:
+            h, out = out[0], out[1:]
+            assert torch.equal(h, (x.float() + res.float()).to(x.dtype))
+        check_rows(*out, h, ref.factors32(d, sn, f32(gain), True), sn, f32(gain), True, eps)
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("rows,d", [(1, 4096), (300, 64), (1000, 2048), (2, 32768), (999, 4096), (400, 32768)])
 def test_rmsnorm_updates_the_residual_stream_in_place(rows, d):
     for alias in ("x", "residual"):
         x, res = values(rows, d, "bf16", 1), values(rows, d, "bf16", 2)
@@ -160,6 +185,12 @@ def test_extreme_magnitudes():
     assert st.item() == 0
     np.testing.assert_array_equal(q.cpu().numpy(), q_want)
     _, scale64 = ref.rows64(rows, None, None, True, eps)
+    many = torch.cat([x] * 50)  # the same rows in a large batch
+    for got_q, got_scale in (qamw.qamw_rmsnorm_int8(many, torch.ones(d, device=DEV), eps),
+                             qamw.qamw_rmsnorm_int8(many, torch.ones(d, device=DEV), eps,
+                                                    residual=torch.zeros_like(many))[1:]):
+        assert torch.equal(got_q, q.repeat(50, 1))
+        assert torch.allclose(got_scale, scale.repeat(50), rtol=64 * U32, atol=0)
     keep = [i for i in range(9) if i != 7]
     got = scale.cpu().numpy().astype(np.float64)
     # the rescaled sum of squares rounds three more times than the 29 of check_rows

@@ -42,265 +42,310 @@ struct Int8RowsArgs {
   int64_t rows;
   int d;
   float eps;
+  float one;   // 1 (see pack_rounded)
   int divide;  // tokens and norm: c = (g or 1) / s, weights: c = s
 };
 
-// Eight consecutive values, as loaded: bf16 in 16 bytes, fp32 in 32.
+// Bound on the row kernels' static shared memory.
+constexpr size_t kStaticRoom = 1024;
+
+// Eight consecutive values, as loaded: bf16 in 16 bytes, fp32 in 32.  LoadOnce
+// is for global data that the call reads once.
 template <typename T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
   uint32_t w[4];
+  __device__ __forceinline__ void set(uint4 u) { w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w; }
+  __device__ __forceinline__ void load_once(const void* p, int64_t vec) {
+    set(__ldcs(reinterpret_cast<const uint4*>(p) + vec));
+  }
   __device__ __forceinline__ void load(const void* p, int64_t vec) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p) + vec);
-    w[0] = u.x;
-    w[1] = u.y;
-    w[2] = u.z;
-    w[3] = u.w;
+    set(reinterpret_cast<const uint4*>(p)[vec]);
   }
-  __device__ __forceinline__ void load_kept(const void* p, int64_t vec) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + vec);
-    w[0] = u.x;
-    w[1] = u.y;
-    w[2] = u.z;
-    w[3] = u.w;
-  }
-  __device__ __forceinline__ float get(int i) const {
-    return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+  __device__ __forceinline__ float2 get(int i) const {  // values 2 i, 2 i + 1
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
   __device__ __forceinline__ void add(const Raw8& o) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = pack_bf16x2(__fadd_rn(get(2 * e), o.get(2 * e)),
-                         __fadd_rn(get(2 * e + 1), o.get(2 * e + 1)));
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = add2(get(i), o.get(i));
+      w[i] = pack_bf16x2(f.x, f.y);
+    }
   }
   __device__ __forceinline__ void store(void* p, int64_t vec) const {
     reinterpret_cast<uint4*>(p)[vec] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
 };
 template <>
 struct Raw8<float> {
-  float f[8];
+  float2 f[4];
   __device__ __forceinline__ void set(float4 a, float4 b) {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
   }
-  __device__ __forceinline__ void load(const void* p, int64_t vec) {
+  __device__ __forceinline__ void load_once(const void* p, int64_t vec) {
     const float4* s = reinterpret_cast<const float4*>(p) + 2 * vec;
     set(__ldcs(s), __ldcs(s + 1));
   }
-  __device__ __forceinline__ void load_kept(const void* p, int64_t vec) {
+  __device__ __forceinline__ void load(const void* p, int64_t vec) {
     const float4* s = reinterpret_cast<const float4*>(p) + 2 * vec;
-    set(__ldg(s), __ldg(s + 1));
+    set(s[0], s[1]);
   }
-  __device__ __forceinline__ float get(int i) const { return f[i]; }
+  __device__ __forceinline__ float2 get(int i) const { return f[i]; }
   __device__ __forceinline__ void add(const Raw8& o) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __fadd_rn(f[e], o.f[e]);
+    for (int i = 0; i < 4; ++i) f[i] = add2(f[i], o.f[i]);
   }
   __device__ __forceinline__ void store(void* p, int64_t vec) const {
     float4* s = reinterpret_cast<float4*>(p) + 2 * vec;
-    s[0] = make_float4(f[0], f[1], f[2], f[3]);
-    s[1] = make_float4(f[4], f[5], f[6], f[7]);
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    s[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    s[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
   }
 };
 
-// The column factors of eight columns.
+// The factors c_j of eight columns.
 template <typename T, bool NORM>
-__device__ __forceinline__ void factors(const Int8RowsArgs& a, int vec, float (&c)[8]) {
+__device__ __forceinline__ void factors(const Int8RowsArgs& a, int vec, float2 (&c)[4]) {
   if constexpr (NORM) {
     Raw8<T> g;
-    g.load_kept(a.gain, vec);
+    g.load(a.gain, vec);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = g.get(e);
+    for (int i = 0; i < 4; ++i) c[i] = g.get(i);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = 1.f;
+    for (int i = 0; i < 4; ++i) c[i] = make_float2(1.f, 1.f);
   }
   if (a.s != nullptr) {
     float s[8];
     load_halves<8>(a.s + 8 * vec, s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = a.divide ? __fdiv_rn(c[e], s[e]) : s[e];
+    for (int i = 0; i < 4; ++i)
+      c[i] = a.divide ? make_float2(__fdiv_rn(c[i].x, s[2 * i]), __fdiv_rn(c[i].y, s[2 * i + 1]))
+                      : make_float2(s[2 * i], s[2 * i + 1]);
   }
 }
 
-// Sum and maximum over the threads of a row (a warp, or the whole CTA).
-struct RowRed {
-  float sum;
-  uint32_t top;
+// max(|a|, |b|, |c|), NaN if one of them is: one instruction for two elements.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A thread's part of a row's statistics: sum of squares (two partial sums) and
+// the largest |v|, NaN when one of the thread's values is.
+struct RowStat {
+  float2 sum;
+  float top;
 };
+
+// v = h c of eight columns into the statistics.
+template <bool NORM, typename T>
+__device__ __forceinline__ void take(RowStat& r, const Raw8<T>& h, const float2 (&c)[4],
+                                     float2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = h.get(i);
+    if constexpr (NORM) r.sum = fma2(f, f, r.sum);
+    v[i] = mul2(f, c[i]);
+    r.top = max3_abs(r.top, v[i].x, v[i].y);
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Scratch of a row's reduction over a CTA (two of them, used in turn: the next
+// row's writes then need no barrier of their own).
+struct RowSlots {
+  uint32_t top[32];
+  float sum[32];
+};
+
+// The row's largest |v| (bits; NaN and Inf are the largest of all) to every
+// thread, its sum of squares to the first warp of the row alone: only the scale
+// depends on it.
 template <bool NORM>
-__device__ __forceinline__ RowRed reduce_row(RowRed r, bool by_warp, RowRed* slots) {
-  if constexpr (NORM) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) r.sum += __shfl_xor_sync(0xffffffffu, r.sum, o);
-  }
-  r.top = __reduce_max_sync(0xffffffffu, r.top);
-  if (by_warp) return r;
+__device__ __forceinline__ uint32_t reduce_row(RowStat r, bool by_warp, RowSlots& slots, float& sum) {
+  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(r.top));
+  if constexpr (NORM) sum = warp_sum(r.sum.x + r.sum.y);
+  if (by_warp) return top;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-  if (lane == 0) slots[warp] = r;
-  __syncthreads();
-  RowRed o;
-  o.sum = 0.f;
-  o.top = 0u;
-  if (lane < nwarps) o = slots[lane];
-  if constexpr (NORM) {
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) o.sum += __shfl_xor_sync(0xffffffffu, o.sum, k);
+  if (lane == 0) {
+    slots.top[warp] = top;
+    if constexpr (NORM) slots.sum[warp] = sum;
   }
-  o.top = __reduce_max_sync(0xffffffffu, o.top);
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, lane < nwarps ? slots.top[lane] : 0u);
+  if constexpr (NORM)
+    if (warp == 0) sum = warp_sum(lane < nwarps ? slots.sum[lane] : 0.f);
+  return top;
+}
+
+// What the rounding of a row needs: 127 / a, or that the row gives q = 0 (below
+// 2^-100, or not finite).
+struct RowOut {
+  float inv;
+  bool some;
+};
+__device__ __forceinline__ RowOut row_out(uint32_t top) {
+  RowOut o;
+  o.some = top < kInfBits && __uint_as_float(top) >= kRowTiny;
+  o.inv = o.some ? __fdiv_rn(kInt8Max, __uint_as_float(top)) : 0.f;
   return o;
 }
 
-// Rows of c in shared memory: eight columns as two float4, 16 bytes apart by
-// half the row, so that a warp's 16-byte loads are consecutive.
-__device__ __forceinline__ void put_factors(float4* tab, int nvec, int v, const float (&c)[8]) {
-  tab[v] = make_float4(c[0], c[1], c[2], c[3]);
-  tab[nvec + v] = make_float4(c[4], c[5], c[6], c[7]);
-}
-__device__ __forceinline__ void get_factors(const float4* tab, int nvec, int v, float (&c)[8]) {
-  const float4 a = tab[v], b = tab[nvec + v];
-  c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
-  c[4] = b.x, c[5] = b.y, c[6] = b.z, c[7] = b.w;
+// The row's scale, by its first warp.  Squares that overflow (|h| beyond about
+// 2^56) are summed again with h 2^-70 from memory, by the warp alone: h is x, or
+// the sum that the row's threads have written ahead of the reduction's barrier.
+constexpr float kDown = 8.470329472543003e-22f;  // 2^-70
+template <typename T, bool NORM>
+__device__ __forceinline__ void put_scale(const Int8RowsArgs& a, int64_t row, uint32_t top, bool some,
+                                          float sum, int lane, int& flags) {
+  float scale = some ? __fdiv_rn(__uint_as_float(top), kInt8Max) : 0.f;
+  if constexpr (NORM) {
+    if (some && !(sum <= FLT_MAX)) {
+      const int nvec = a.d / 8;
+      const void* h = a.sum != nullptr ? a.sum : a.x;
+      float2 w = make_float2(0.f, 0.f);
+      for (int v = lane; v < nvec; v += 32) {
+        Raw8<T> r;
+        r.load(h, row * nvec + v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = mul2(r.get(i), make_float2(kDown, kDown));
+          w = fma2(f, f, w);
+        }
+      }
+      scale = scale * kDown * (1.f / sqrtf(warp_sum(w.x + w.y) / (float)a.d));
+    } else {
+      scale *= 1.f / sqrtf(sum / (float)a.d + a.eps);
+    }
+  }
+  const bool finite = top < kInfBits;
+  if (lane == 0) {
+    a.scale[row] = finite ? scale : __uint_as_float(0x7fc00000u);
+    if (!finite) flags |= QAMW_STATUS_NONFINITE;
+  }
 }
 
-// Four rounded values as the bytes of a word.  x + 1.5 2^23 rounds x to a whole
-// number (ties to even) whose low byte is the low byte of the sum's pattern: an
-// addition in place of a conversion, which has a quarter of its rate.
-__device__ __forceinline__ uint32_t pack_rounded(float a, float b, float c, float d) {
-  constexpr float kMagic = 12582912.f;
-  const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(a, kMagic)),
-                                  __float_as_uint(__fadd_rn(b, kMagic)), 0x0040);
-  const uint32_t hi = __byte_perm(__float_as_uint(__fadd_rn(c, kMagic)),
-                                  __float_as_uint(__fadd_rn(d, kMagic)), 0x0040);
+// Four products v inv rounded to the bytes of a word.  x + 1.5 2^23 rounds x to a
+// whole number (ties to even) whose low byte is the low byte of the sum's
+// pattern: an addition in place of a conversion, which has a quarter of its
+// rate.  The product has to be rounded first; a packed addition behind it gets
+// fused with it, so the addition is fma(x, one, 1.5 2^23) with a `one` that the
+// compiler does not know.
+__device__ __forceinline__ uint32_t pack_rounded(float2 a, float2 b, float2 inv, float2 one) {
+  const float2 magic = make_float2(12582912.f, 12582912.f);
+  a = fma2(mul2(a, inv), one, magic);
+  b = fma2(mul2(b, inv), one, magic);
+  const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
   return __byte_perm(lo, hi, 0x5410);
 }
 
+// Eight values v_j into the row's q at vector `at`.
+__device__ __forceinline__ void put_q(const Int8RowsArgs& a, int64_t at, const float2 (&v)[4],
+                                      const RowOut& o) {
+  const float2 inv = make_float2(o.inv, o.inv), one = make_float2(a.one, a.one);
+  reinterpret_cast<uint2*>(a.q)[at] =
+      make_uint2(pack_rounded(v[0], v[1], inv, one), pack_rounded(v[2], v[3], inv, one));
+}
+
 // How a row is shared out (MODE) and where its thread keeps c_j:
-//   kWarpRow  a warp per row, eight rows a CTA (d <= 1024); c in registers;
+//   kWarpRow  a warp per row, eight rows a CTA (d <= 512); c in registers;
 //   kWideRow  a CTA per row, one vector of eight columns a thread; c in
 //             registers: the shortest chain for a few rows;
-//   kDeepRow  a CTA per row, VEC vectors a thread; c in shared memory, so that
-//             the registers allow about a thousand threads per SM, each with
-//             VEC loads per input in flight.
+//   kDeepRow  a CTA per row, four vectors a thread; c in shared memory (as two
+//             arrays of float4, so that a warp's loads are consecutive): rows
+//             too long for the ring below.
 enum { kWarpRow, kWideRow, kDeepRow };
 
 template <typename T, int MODE, int VEC, bool NORM, bool RES>
 __global__ void __launch_bounds__(MODE == kWarpRow ? 256 : 1024, 1)
     k_int8_rows(const Int8RowsArgs a) {
-  __shared__ RowRed slots[2][32];
+  __shared__ RowSlots slots[2];
   extern __shared__ __align__(16) float4 c_tab[];
-  constexpr bool kByWarp = MODE == kWarpRow;
+  constexpr bool kByWarp = MODE == kWarpRow, kTable = MODE == kDeepRow;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = kByWarp ? 32 : blockDim.x;
-  const int t = kByWarp ? (threadIdx.x & 31) : threadIdx.x;
+  const int t = kByWarp ? lane : threadIdx.x;
   const int nvec = a.d / 8;
   const int64_t groups = kByWarp ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
-  const int64_t first =
-      kByWarp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t first = kByWarp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
   pdl_wait();
   pdl_trigger();
-  float c[MODE == kDeepRow ? 1 : VEC][8];
-  if constexpr (MODE == kDeepRow) {
+  float2 c[kTable ? 1 : VEC][4];
+  if constexpr (kTable) {
     for (int v = t; v < nvec; v += n) {  // each thread reads back what it wrote
       factors<T, NORM>(a, v, c[0]);
-      put_factors(c_tab, nvec, v, c[0]);
+      c_tab[v] = make_float4(c[0][0].x, c[0][0].y, c[0][1].x, c[0][1].y);
+      c_tab[nvec + v] = make_float4(c[0][2].x, c[0][2].y, c[0][3].x, c[0][3].y);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       if (t + i * n < nvec) factors<T, NORM>(a, t + i * n, c[i]);
   }
+  const auto from_table = [&](int v) {
+    const float4 p = c_tab[v], q = c_tab[nvec + v];
+    c[0][0] = make_float2(p.x, p.y), c[0][1] = make_float2(p.z, p.w);
+    c[0][2] = make_float2(q.x, q.y), c[0][3] = make_float2(q.z, q.w);
+  };
   int flags = 0, parity = 0;
   for (int64_t row = first; row < a.rows; row += groups) {
     const int64_t base = row * nvec;
     Raw8<T> h[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int v = t + i * n;
-      h[i].zero();
-      if (v < nvec) h[i].load(a.x, base + v);
-    }
+    for (int i = 0; i < VEC; ++i)
+      if (t + i * n < nvec) h[i].load_once(a.x, base + t + i * n);
     if constexpr (RES) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const int v = t + i * n;
         if (v < nvec) {
           Raw8<T> r;
-          r.load(a.res, base + v);
+          r.load_once(a.res, base + v);
           h[i].add(r);
         }
       }
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int v = t + i * n;
-        if (v < nvec) h[i].store(a.sum, base + v);
-      }
+      for (int i = 0; i < VEC; ++i)
+        if (t + i * n < nvec) h[i].store(a.sum, base + t + i * n);
     }
-    RowRed r;
-    r.sum = 0.f;
-    r.top = 0u;
+    RowStat r;
+    r.sum = make_float2(0.f, 0.f);
+    r.top = 0.f;
+    float2 v[4];
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
       if (t + i * n < nvec) {
-        if constexpr (MODE == kDeepRow) get_factors(c_tab, nvec, t + i * n, c[0]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float f = h[i].get(e);
-          if constexpr (NORM) r.sum = fmaf(f, f, r.sum);
-          r.top = max(r.top, __float_as_uint(fabsf(__fmul_rn(f, c[MODE == kDeepRow ? 0 : i][e]))));
-        }
+        if constexpr (kTable) from_table(t + i * n);
+        take<NORM>(r, h[i], c[kTable ? 0 : i], v);
       }
-    r = reduce_row<NORM>(r, kByWarp, slots[parity]);
+    float sum = 0.f;
+    const uint32_t top = reduce_row<NORM>(r, kByWarp, slots[parity], sum);
     parity ^= 1;
-    const float top = __uint_as_float(r.top);
-    const bool finite = r.top < kInfBits, some = finite && top >= kRowTiny;
-    const float inv = some ? __fdiv_rn(kInt8Max, top) : 0.f;
-    float scale = some ? __fdiv_rn(top, kInt8Max) : 0.f;
-    if constexpr (NORM) {
-      if (some && r.sum > FLT_MAX) {
-        // the squares overflow (|h| beyond about 2^56): again with h 2^-70, whose
-        // squares fit; what underflows there is far below the row's largest
-        RowRed w;
-        w.sum = 0.f;
-        w.top = 0u;
+    const RowOut o = row_out(top);
+    if (kByWarp || warp == 0) {
+      __syncwarp();  // by_warp: the lanes' sums are written before one of them reads
+      put_scale<T, NORM>(a, row, top, o.some, sum, lane, flags);
+    }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
+    for (int i = 0; i < VEC; ++i)
+      if (t + i * n < nvec) {
+        if constexpr (kTable) from_table(t + i * n);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float f = h[i].get(e) * 8.470329472543003e-22f;
-            w.sum = fmaf(f, f, w.sum);
-          }
-        w = reduce_row<NORM>(w, kByWarp, slots[parity]);
-        parity ^= 1;
-        scale = scale * 8.470329472543003e-22f * (1.f / sqrtf(w.sum / (float)a.d));
-      } else {
-        scale *= 1.f / sqrtf(r.sum / (float)a.d + a.eps);
+        for (int e = 0; e < 4; ++e) v[e] = mul2(h[i].get(e), c[kTable ? 0 : i][e]);
+        if (o.some)
+          put_q(a, base + t + i * n, v, o);
+        else
+          reinterpret_cast<uint2*>(a.q)[base + t + i * n] = make_uint2(0u, 0u);
       }
-    }
-    if (t == 0) {
-      a.scale[row] = finite ? scale : __uint_as_float(0x7fc00000u);
-      if (!finite) flags |= QAMW_STATUS_NONFINITE;
-    }
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const int v = t + i * n;
-      if (v < nvec) {
-        if constexpr (MODE == kDeepRow) get_factors(c_tab, nvec, v, c[0]);
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          f[e] = __fmul_rn(__fmul_rn(h[i].get(e), c[MODE == kDeepRow ? 0 : i][e]), inv);
-        uint2 w = make_uint2(pack_rounded(f[0], f[1], f[2], f[3]), pack_rounded(f[4], f[5], f[6], f[7]));
-        if (!some) w = make_uint2(0u, 0u);
-        reinterpret_cast<uint2*>(a.q)[base + v] = w;
-      }
-    }
   }
   raise_flag(a.status, flags);
 }
@@ -309,7 +354,8 @@ template <typename T, int MODE, int VEC, bool NORM, bool RES>
 cudaError_t run_rows(const Int8RowsArgs& a, int threads, cudaStream_t stream) {
   auto fn = &k_int8_rows<T, MODE, VEC, NORM, RES>;
   const size_t smem = MODE == kDeepRow ? (size_t)a.d * sizeof(float) : 0;
-  cudaError_t err = allow_smem(reinterpret_cast<const void*>(fn), smem);
+  // the opt-in is for static and dynamic together above 48 KB: asked for with room
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(fn), smem + kStaticRoom);
   if (err != cudaSuccess) return err;
   const int64_t per = MODE == kWarpRow ? threads / 32 : 1;
   const int grid =
@@ -317,19 +363,159 @@ cudaError_t run_rows(const Int8RowsArgs& a, int threads, cudaStream_t stream) {
   return launch_pdl(fn, dim3(grid), dim3(threads), smem, stream, a);
 }
 
+// Many rows: a CTA per row again, its inputs brought into a ring of `stages`
+// rows in shared memory by bulk copies, so that about 200 KB per SM are in
+// flight whatever the rows' threads are waiting for.  Two vectors a thread; c
+// and, between the reduction and the rounding, v in registers.  The reduction's
+// barrier also says that every thread has read the row, so the stage is refilled
+// right behind it.  The last warp has no vectors: it issues the copies and forms
+// the scales (a chain of divisions and a root, some 300 cycles) while the others
+// go on to the next row.
+constexpr int kRingVec = 2;
+constexpr int kRingMax = 8;
+// Threads of a CTA at most; fewer with fp32 and a residual (d <= 13312 then),
+// which needs more than 64 registers.
+template <typename T, bool RES>
+constexpr int ring_threads() {
+  return RES && sizeof(T) == 4 ? 864 : 1024;
+}
+
+template <typename T, bool NORM, bool RES>
+__global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
+    k_int8_ring(const Int8RowsArgs a, int stages) {
+  __shared__ RowSlots slots[2];
+  __shared__ uint64_t full[kRingMax];
+  extern __shared__ __align__(128) unsigned char ring[];
+  const int n = blockDim.x - 32, t = threadIdx.x, nvec = a.d / 8;
+  const int lane = t & 31, warp = t >> 5, nwarps = n >> 5;
+  const uint32_t row_bytes = (uint32_t)a.d * sizeof(T), stage = row_bytes * (RES ? 2 : 1);
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  int flags = 0, parity = 0, s = 0;
+  if (warp == nwarps) {
+    const auto fetch = [&](int64_t row, int s) {
+      if (row >= a.rows) return;
+      unsigned char* dst = ring + (size_t)s * stage;
+      mbar_expect_tx(&full[s], stage);
+      bulk_g2s(dst, static_cast<const unsigned char*>(a.x) + row * row_bytes, row_bytes, &full[s]);
+      if constexpr (RES)
+        bulk_g2s(dst + row_bytes, static_cast<const unsigned char*>(a.res) + row * row_bytes,
+                 row_bytes, &full[s]);
+    };
+    if (lane == 0)
+      for (int j = 0; j < stages; ++j) fetch(blockIdx.x + (int64_t)j * gridDim.x, j);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+      __syncthreads();
+      if (lane == 0) fetch(row + (int64_t)stages * gridDim.x, s);
+      const RowSlots& r = slots[parity];
+      const uint32_t top = __reduce_max_sync(0xffffffffu, lane < nwarps ? r.top[lane] : 0u);
+      const float sum = NORM ? warp_sum(lane < nwarps ? r.sum[lane] : 0.f) : 0.f;
+      put_scale<T, NORM>(a, row, top, row_out(top).some, sum, lane, flags);
+      parity ^= 1;
+      if (++s == stages) s = 0;
+    }
+  } else {
+    float2 c[kRingVec][4];
+#pragma unroll
+    for (int i = 0; i < kRingVec; ++i)
+      if (t + i * n < nvec) factors<T, NORM>(a, t + i * n, c[i]);
+    uint32_t u = 0;
+    bool alive = true;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+      const int64_t base = row * nvec;
+      // a wait that gives up is not repeated; the row's barriers are still met
+      if (alive && !mbar_wait_bounded(&full[s], u & 1u)) {
+        alive = false;
+        flags |= QAMW_STATUS_TIMEOUT;
+      }
+      const unsigned char* src = ring + (size_t)s * stage;
+      float2 v[kRingVec][4];
+      RowStat r;
+      r.sum = make_float2(0.f, 0.f);
+      r.top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRingVec; ++i) {
+        const int at = t + i * n;
+        if (at < nvec) {
+          Raw8<T> h;
+          h.load(src, at);
+          if constexpr (RES) {
+            Raw8<T> o;
+            o.load(src + row_bytes, at);
+            h.add(o);
+            h.store(a.sum, base + at);
+          }
+          take<NORM>(r, h, c[i], v[i]);
+        }
+      }
+      RowSlots& slot = slots[parity];
+      uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(r.top));
+      float sum = 0.f;
+      if constexpr (NORM) sum = warp_sum(r.sum.x + r.sum.y);
+      if (lane == 0) {
+        slot.top[warp] = top;
+        if constexpr (NORM) slot.sum[warp] = sum;
+      }
+      __syncthreads();
+      top = __reduce_max_sync(0xffffffffu, lane < nwarps ? slot.top[lane] : 0u);
+      parity ^= 1;
+      const RowOut o = row_out(top);
+      if (o.some) {
+#pragma unroll
+        for (int i = 0; i < kRingVec; ++i)
+          if (t + i * n < nvec) put_q(a, base + t + i * n, v[i], o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRingVec; ++i)
+          if (t + i * n < nvec) reinterpret_cast<uint2*>(a.q)[base + t + i * n] = make_uint2(0u, 0u);
+      }
+      if (++s == stages) {
+        s = 0;
+        ++u;
+      }
+    }
+  }
+  raise_flag(a.status, flags);
+}
+
+// Shared memory of an SM that the rings of its CTAs (about 1024 threads together)
+// take: 104 KB in flight were as fast as it got (208 KB: 8192 x 5120 bf16 with
+// residual 53.5 us against 48.9), but a ring has two rows at least.
+constexpr size_t kRingBytes = 104 * 1024, kRingMost = 208 * 1024;
+
+template <typename T, bool NORM, bool RES>
+cudaError_t run_ring(const Int8RowsArgs& a, int threads, int stages, size_t smem,
+                     cudaStream_t stream) {
+  auto fn = &k_int8_ring<T, NORM, RES>;
+  // the opt-in is for static and dynamic together above 48 KB: asked for with room
+  cudaError_t err = allow_smem(reinterpret_cast<const void*>(fn), smem + kStaticRoom);
+  if (err != cudaSuccess) return err;
+  const int grid = persistent_grid(reinterpret_cast<const void*>(fn), threads, smem, a.rows);
+  return launch_pdl(fn, dim3(grid), dim3(threads), smem, stream, a, stages);
+}
+
 template <typename T, bool NORM, bool RES>
 cudaError_t run_rows_any(const Int8RowsArgs& a, cudaStream_t stream) {
   const int nvec = a.d / 8;
-  if (a.d <= 1024) {
+  if (a.d <= 512) {
     const int threads = (int)std::min<int64_t>(8, a.rows) * 32;
-    switch ((nvec + 31) / 32) {
-      case 1: return run_rows<T, kWarpRow, 1, NORM, RES>(a, threads, stream);
-      case 2: return run_rows<T, kWarpRow, 2, NORM, RES>(a, threads, stream);
-      default: return run_rows<T, kWarpRow, 4, NORM, RES>(a, threads, stream);
-    }
+    return nvec <= 32 ? run_rows<T, kWarpRow, 1, NORM, RES>(a, threads, stream)
+                      : run_rows<T, kWarpRow, 2, NORM, RES>(a, threads, stream);
   }
   if (a.rows <= 2 * sm_count() && nvec <= 1024)
     return run_rows<T, kWideRow, 1, NORM, RES>(a, (nvec + 31) / 32 * 32, stream);
+  const size_t stage = (size_t)a.d * sizeof(T) * (RES ? 2 : 1);
+  const int threads = ((nvec + kRingVec - 1) / kRingVec + 31) / 32 * 32 + 32;
+  if (threads <= ring_threads<T, RES>() && 2 * stage <= kRingMost) {
+    const size_t per = kRingBytes / std::max(1, 1024 / threads);
+    const int stages = (int)std::min<size_t>(kRingMax, std::max<size_t>(2, per / stage));
+    return run_ring<T, NORM, RES>(a, threads, stages, stages * stage, stream);
+  }
   return run_rows<T, kDeepRow, 4, NORM, RES>(a, ((nvec + 3) / 4 + 31) / 32 * 32, stream);
 }
 
@@ -339,6 +525,7 @@ cudaError_t launch_int8_encode(const void* d_x, int dtype, int64_t rows, int d,
                                const uint16_t* d_chan_scale, bool divide, int8_t* d_q,
                                float* d_scale, int32_t* d_status, cudaStream_t stream) {
   Int8RowsArgs a = {};
+  a.one = 1.f;
   a.x = d_x;
   a.s = reinterpret_cast<const __half*>(d_chan_scale);
   a.q = d_q;
@@ -356,6 +543,7 @@ cudaError_t launch_rmsnorm_int8(const void* d_x, const void* d_residual, int dty
                                 const uint16_t* d_chan_scale, void* d_sum, int8_t* d_q,
                                 float* d_scale, int32_t* d_status, cudaStream_t stream) {
   Int8RowsArgs a = {};
+  a.one = 1.f;
   a.x = d_x;
   a.res = d_residual;
   a.gain = d_gain;
