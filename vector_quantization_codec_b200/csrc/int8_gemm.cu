@@ -10,6 +10,9 @@
 // 32, and the 32 lanes of an epilogue warp store 32 consecutive outputs of a
 // token whatever d_out is.
 #include <algorithm>
+#include <climits>
+#include <cstdio>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -23,10 +26,13 @@ constexpr int kRowsM = 128;           // output channels per CTA
 constexpr int kChunk = 128;           // bytes of a row per stage: one swizzled line
 constexpr uint32_t kTileA = kRowsM * kChunk;
 constexpr int kMaxStages = 12;
-constexpr int kEpiWarps = 4;          // warps 0-3: one tensor-memory lane quarter each
-constexpr int kMmaWarp = 4;           // owner of the tensor memory; lane 0 issues the MMAs
-constexpr int kCopyWarp = 5;          // lane 0 issues the copies
-constexpr int kThreads = 6 * 32;
+constexpr int kEpiWarps = 8;          // warps 0-7: two per tensor-memory lane quarter
+constexpr int kMmaWarp = 8;           // owner of the tensor memory; one thread issues the MMAs
+constexpr int kCopyWarp = 9;          // one thread issues the copies
+constexpr int kThreads = 10 * 32;
+
+constexpr uint32_t kRing = 216u * 1024u;  // shared memory of the stages
+constexpr int kMaxSplits = 8;             // CTAs of a cluster
 
 struct Int8GemmArgs {
   const float* xs;
@@ -127,15 +133,15 @@ __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t da, uint64_t db, uin
         : "memory");
 }
 
-// Arrive on `bar` (CG 2: on the barrier at that offset of the CTAs in `ctas`)
-// once every MMA issued so far is done.
+// Arrive on `bar` (CG 2: on the barrier at that offset of the cluster's CTAs in
+// the mask `ctas`) once every MMA issued so far is done.
 template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar, uint16_t ctas = 3) {
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t ctas) {
   if constexpr (CG == 2)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)),
-        "h"(ctas)
+        "h"((uint16_t)ctas)
         : "memory");
   else
     tc_commit(bar);
@@ -191,40 +197,42 @@ __host__ __device__ inline uint32_t tmem_cols(int nt) {
   return c;
 }
 
-// Sum of the S partial tiles [token][128 channels] of a cluster: CTA `rank`
-// adds up and writes tokens rank, rank + S, ..., a warp one token at a time, a
-// lane four channels; the loads of kAhead tokens from all S CTAs are in flight
-// together (one distributed shared-memory latency instead of one per token).
-template <int S, typename T>
-__device__ __forceinline__ void add_partials(const Int8GemmArgs& a, int64_t tile, uint32_t rank,
-                                             uint32_t part, int warp, int lane) {
-  constexpr int kAhead = 8 / S > 2 ? 8 / S : 2;
+// Sum of the `splits` partial tiles [token][128 channels] of a cluster: CTA
+// `split` adds up and writes tokens split, split + splits, ..., of its 128
+// channels, a warp one token at a time, a lane four channels; the loads of two
+// tokens from all CTAs are in flight together.  The CTAs with the same channels
+// have the cluster ranks r0, r0 + CG, ...
+template <int CG, typename T>
+__device__ __forceinline__ void add_partials(const Int8GemmArgs& a, int64_t i, int t0, int split,
+                                             uint32_t r0, uint32_t part, int warp, int lane) {
+  constexpr int kAhead = 2;
+  constexpr int kMost = kMaxSplits / CG;
   T* y = reinterpret_cast<T*>(a.y);
-  const int64_t m = tile / a.tok_tiles;
-  const int64_t i = m * kRowsM + 4 * lane;
-  const int t0 = (int)(tile - m * a.tok_tiles) * a.nt;
-  const int nt = min(a.nt, a.ntok - t0);
+  const int nt = min(a.nt, a.ntok - t0), stride = a.splits * kEpiWarps;
+  i += 4 * lane;
   float w[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) w[e] = i + e < a.d_out ? __ldg(a.ws + i + e) : 0.f;
-  uint32_t from[S];
+  uint32_t from[kMost];
 #pragma unroll
-  for (int r = 0; r < S; ++r) from[r] = cluster_addr(part + 16u * lane, (uint32_t)r);
-  for (int c0 = (int)rank + S * warp; c0 < nt; c0 += S * kEpiWarps * kAhead) {
-    int4 v[kAhead][S];
+  for (int r = 0; r < kMost; ++r)
+    from[r] = cluster_addr(part + 16u * lane, r0 + (uint32_t)(CG * min(r, a.splits - 1)));
+  for (int c0 = split + a.splits * warp; c0 < nt; c0 += stride * kAhead) {
+    int4 v[kAhead][kMost];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int c = min(c0 + j * S * kEpiWarps, a.nt - 1);
+      const uint32_t at = 4u * kRowsM * (uint32_t)min(c0 + j * stride, a.nt - 1);
 #pragma unroll
-      for (int r = 0; r < S; ++r) v[j][r] = lds_cluster(from[r] + 4u * kRowsM * (uint32_t)c);
+      for (int r = 0; r < kMost; ++r)
+        v[j][r] = r < a.splits ? lds_cluster(from[r] + at) : make_int4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int c = c0 + j * S * kEpiWarps;
+      const int c = c0 + j * stride;
       if (c >= nt) break;
       int sum[4] = {};
 #pragma unroll
-      for (int r = 0; r < S; ++r) {
+      for (int r = 0; r < kMost; ++r) {
         sum[0] += v[j][r].x;
         sum[1] += v[j][r].y;
         sum[2] += v[j][r].z;
@@ -239,12 +247,13 @@ __device__ __forceinline__ void add_partials(const Int8GemmArgs& a, int64_t tile
   }
 }
 
-// CG = 2: a cluster of two CTAs works on a tile of 256 output channels (128 in
-// each CTA's tensor memory) and nt tokens, each CTA staging its own 128 rows of
-// W and half of the tokens; the even CTA (leader) issues the MMAs of both.
-// CG = 1: a tile of 128 channels per CTA, or per cluster of `splits` CTAs that
-// share the chunks of the tile and add their integer partial sums through
-// distributed shared memory.
+// CG = 2: a pair of CTAs works on a tile of 256 output channels (128 in each
+// CTA's tensor memory) and nt tokens, each CTA staging its own 128 rows of W and
+// half of the tokens; the even CTA (leader) issues the MMAs of both.
+// CG = 1: a tile of 128 channels per CTA.
+// With splits > 1 a cluster of that many CTAs or pairs shares the chunks of one
+// tile and adds its integer partial sums through distributed shared memory; else
+// the CTAs or pairs are persistent over tiles.
 // Roles meet at mbarriers only: copies fill a ring of stages (full / empty), the
 // MMAs fill one of two accumulators (accfull / accempty), the epilogue warps
 // read the other out.
@@ -258,14 +267,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) float xs_tile[kEpiWarps][256];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const uint32_t rank = CG == 2 || a.splits > 1 ? cluster_rank() : 0u;
+  const uint32_t crank = CG == 2 || a.splits > 1 ? cluster_rank() : 0u;
+  // place in the pair, split of the tile's chunks, the pair's leader and mask
+  const uint32_t rank = CG == 2 ? (crank & 1u) : 0u;
+  const int split = (int)(crank / CG);
+  const uint32_t leader = crank - rank, pair = 3u << leader;
   const int S = a.stages;
   const uint32_t box = box_bytes(CG, a.nt), stage = box * a.boxes, cols = tmem_cols(a.nt);
   // tiles of this CTA (pair, cluster): first, first + step, ...
-  const int per = CG == 2 ? 2 : a.splits;
+  const int per = CG * a.splits;
   const int64_t first = blockIdx.x / per, step = gridDim.x / per;
-  const int c_lo = CG == 2 ? 0 : (int)((int64_t)rank * a.chunks / a.splits);
-  const int c_hi = CG == 2 ? a.chunks : (int)((int64_t)(rank + 1) * a.chunks / a.splits);
+  const int c_lo = (int)((int64_t)split * a.chunks / a.splits);
+  const int c_hi = (int)((int64_t)(split + 1) * a.chunks / a.splits);
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (CG == 1 || rank == 0) mbar_expect_tx(&full[s], box * CG * nb);
-          const uint32_t bar = CG == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+          const uint32_t bar = CG == 2 ? cluster_addr(smem_u32(&full[s]), leader) : smem_u32(&full[s]);
           uint32_t dst = smem_u32(smem) + (uint32_t)s * stage;
           for (int j = 0; j < nb; ++j, dst += box) {
             copy_box<CG>(dst, &map_w, (c + j) * kChunk, row, bar);
@@ -363,28 +376,30 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (k < steps)
                 mma_i8<CG>(d, da + 2u * k, db + 2u * k, idesc, (c + j > c_lo || k > 0) ? 1u : 0u);
           }
-          commit<CG>(&empty[s]);
+          commit<CG>(&empty[s], pair);
           if (++s == S) {
             s = 0;
             ++u;
           }
         }
-        if (ok) commit<CG>(&accfull[b]);
+        if (ok) commit<CG>(&accfull[b], pair);
       }
       if (!ok) flags |= QAMW_STATUS_TIMEOUT;
       // every MMA is done before the tensor memory and the stages are given up
-      commit<CG>(&fin, 1);
+      commit<CG>(&fin, 1u << leader);
       if (!mbar_wait_bounded(&fin, 0)) flags |= QAMW_STATUS_TIMEOUT;
     }
-  } else if (CG == 2 || a.splits == 1) {
+  } else if (a.splits == 1) {
     T* y = reinterpret_cast<T*>(a.y);
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
+    // warp w: lanes (channels) 32 (w % 4) .. + 31, columns 16 (w / 4) + 32 k .. + 15
+    const int q4 = warp & 3, half = warp >> 2;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     float* xs = xs_tile[warp];
     int n = 0;
     for (int64_t tile = first; tile < a.tiles; tile += step, ++n) {
       const int b = n & 1;
       const int64_t m = tile / a.tok_tiles;
-      const int64_t i = m * (kRowsM * CG) + (CG == 2 ? (int64_t)rank * kRowsM : 0) + 32 * warp + lane;
+      const int64_t i = m * (kRowsM * CG) + (CG == 2 ? (int64_t)rank * kRowsM : 0) + 32 * q4 + lane;
       const int t0 = (int)(tile - m * a.tok_tiles) * a.nt;
       const int nt = min(a.nt, a.ntok - t0);
       const bool mine = i < a.d_out;
@@ -397,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      T* out = y + (int64_t)t0 * a.d_out + i;
       const int64_t pitch = a.d_out;
-      for (int c = 0; c < nt; c += 16, out += 16 * pitch) {
+      T* out = y + (t0 + 16 * half) * pitch + i;
+      for (int c = 16 * half; c < nt; c += 32, out += 32 * pitch) {
         int v[16];
         tmem_ld16(lane_base + (uint32_t)(b * a.nt + c), v);
         float f[16];
@@ -420,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         if (CG == 2)
-          mbar_arrive_cluster(cluster_addr(smem_u32(&accempty[b]), 0));
+          mbar_arrive_cluster(cluster_addr(smem_u32(&accempty[b]), leader));
         else
           mbar_arrive(&accempty[b]);
       }
@@ -432,24 +447,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool ok = lane != 0 || mbar_wait_bounded(&accfull[0], 0);
     if (__any_sync(0xffffffffu, !ok)) flags |= QAMW_STATUS_TIMEOUT;
     tc_fence_after();
-    for (int c = 0; c < a.nt; c += 16) {
+    for (int c = 16 * (warp >> 2); c < a.nt; c += 32) {
       int v[16];
-      tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)c, v);
+      tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, v);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) part[(c + e) * kRowsM + tid] = v[e];
+      for (int e = 0; e < 16; ++e) part[(c + e) * kRowsM + (tid & (kRowsM - 1))] = v[e];
     }
   }
   tc_fence_before();
-  if (CG == 1 && a.splits > 1) {
+  if (a.splits > 1) {
     __syncwarp();
     cluster_sync();
     if (warp < kEpiWarps) {
-      if (a.splits == 2)
-        add_partials<2, T>(a, first, rank, smem_u32(smem), warp, lane);
-      else if (a.splits == 4)
-        add_partials<4, T>(a, first, rank, smem_u32(smem), warp, lane);
-      else
-        add_partials<8, T>(a, first, rank, smem_u32(smem), warp, lane);
+      const int64_t m = first / a.tok_tiles;
+      add_partials<CG, T>(a, m * (kRowsM * CG) + (int64_t)rank * kRowsM,
+                          (int)(first - m * a.tok_tiles) * a.nt, split, rank, smem_u32(smem), warp,
+                          lane);
     }
   }
   __syncwarp();
@@ -481,37 +494,69 @@ struct Int8Plan {
   int cg, nt, splits, boxes, stages;
 };
 
+// Estimated time (ns) of a plan, fitted to 350 measured (shape, plan) pairs from
+// 1 x 512 -> 1000 to 3000 x 4096 -> 11008; over those 24 shapes the plan that it
+// picks is within 3% of the fastest one measured.  A chunk of a CTA costs the
+// longest of its MMAs, its way through shared memory (128 channels and nt / cg
+// tokens) and a floor; the last tile's epilogue is not hidden, earlier ones are
+// unless the depth is short; sharing a tile's chunks among CTAs costs two
+// cluster barriers and the reading of the partial sums.
+int plan_ns(int ntok, int d_out, int chunks, int cg, int nt, int splits, int sms) {
+  const int64_t tiles =
+      (int64_t)((d_out + kRowsM * cg - 1) / (kRowsM * cg)) * ((ntok + nt - 1) / nt);
+  const int at_once = std::max(1, sms / (cg * splits));
+  const int64_t waves = (tiles + at_once - 1) / at_once;
+  const int chunk = std::max(std::max(118 * nt / 100, 87 * (kRowsM + nt / cg) / 100), 197);
+  const int main = (chunks + splits - 1) / splits * chunk, epilogue = 11 * nt;
+  int64_t t = waves * (std::max(main, epilogue) + 1500) + epilogue;
+  if (splits > 1) t += waves * 4300 + (waves - 1) * epilogue + 7 * nt;
+  return (int)std::min<int64_t>(t, INT_MAX);
+}
+
 Int8Plan plan_int8(int ntok, int d_out, int d_in) {
-  Int8Plan p;
-  const int chunks = (d_in + kChunk - 1) / kChunk;
-  p.splits = 1;
-  if (ntok <= 128) {
-    p.cg = 1;
-    p.nt = (ntok + 15) / 16 * 16;
-    const int tiles = (d_out + kRowsM - 1) / kRowsM;
-    while (p.splits < 8 && tiles * p.splits * 2 <= sm_count() && chunks >= p.splits * 4) p.splits *= 2;
-  } else {
-    p.cg = 2;
-    p.nt = 256;
+  Int8Plan p = {};
+  const int chunks = (d_in + kChunk - 1) / kChunk, sms = sm_count();
+  int best = INT_MAX;
+  for (int cg = 1; cg <= 2; ++cg) {
+    // tokens in steps of 16 per CTA; single CTAs only where a pair's tile would be
+    // wider than the batch needs
+    const int unit = 16 * cg, most = cg == 1 ? 128 : 256;
+    if (cg == 1 && ntok > 512) continue;
+    for (int nt = unit; nt <= most && nt < ntok + unit; nt += unit)
+      for (int splits = 1; splits * cg <= kMaxSplits; ++splits) {
+        if (splits > 1 && 2 * splits > chunks) break;
+        if (splits * cg == 5 || splits * cg == 7) continue;  // leave SMs of a GPC unused
+        const int t = plan_ns(ntok, d_out, chunks, cg, nt, splits, sms);
+        if (t < best) {
+          best = t;
+          p.cg = cg;
+          p.nt = nt;
+          p.splits = splits;
+        }
+      }
   }
+  int ovb = 0, ovr = 0; if (const char* e = getenv("QI8")) sscanf(e, "%d,%d,%d,%d,%d", &p.cg, &p.nt, &p.splits, &ovb, &ovr);
   // the wait for a stage and its commit cost the MMA thread about 240 cycles:
   // several chunks per stage, as long as three stages fit
-  constexpr uint32_t kRing = 218u * 1024u;
+  const uint32_t ring = kRing;
   p.boxes = 4;
-  while (p.boxes > 1 && kRing / (box_bytes(p.cg, p.nt) * p.boxes) < 3) p.boxes /= 2;
-  p.stages = (int)std::min<uint32_t>(kMaxStages, kRing / (box_bytes(p.cg, p.nt) * p.boxes));
+  while (p.boxes > 1 && ring / (box_bytes(p.cg, p.nt) * p.boxes) < 3) p.boxes /= 2;
+  if (ovb) p.boxes = ovb;
+  p.stages = (int)std::min<uint32_t>(kMaxStages, ring / (box_bytes(p.cg, p.nt) * p.boxes));
   return p;
 }
 
 template <int CG, typename T>
 cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap& mx,
                      const Int8GemmArgs& a, cudaStream_t stream) {
-  // at least 116 KB, so that no two CTAs that own tensor memory share an SM
-  const size_t smem = std::max<size_t>((size_t)p.stages * p.boxes * box_bytes(p.cg, p.nt) + 1024, 116 * 1024);
   auto fn = &k_int8_gemm<CG, T>;
+  // all of the ring, whatever the stages need of it: one CTA that owns tensor
+  // memory per SM, so that an allocation never waits for a CTA that could be
+  // waiting for it
+  constexpr size_t smem = kRing + 1024;
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(fn), smem);
   if (err != cudaSuccess) return err;
-  const int per = CG == 2 ? 2 : p.splits;
+  const int per = CG * p.splits;
   const int64_t most = p.splits > 1 ? a.tiles : std::max(1, sm_count() / per);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(std::min<int64_t>(a.tiles, most) * per));
