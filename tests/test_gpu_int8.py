@@ -227,7 +227,7 @@ TOKENS = [1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 31, 33, 64, 65, 100, 128, 129, 200, 2
 
 @pytest.mark.parametrize("ntok", TOKENS)
 def test_gemm_token_counts(ntok):
-    for d_out, d_in in ((300, 1024), (129, 192)):
+    for d_out, d_in in ((300, 1024), (129, 192), (328, 512), (200, 64)):
         check_gemm(ints(ntok, d_in, ntok), scales(ntok, 1), ints(d_out, d_in, 3), scales(d_out, 2),
                    torch.bfloat16)
 

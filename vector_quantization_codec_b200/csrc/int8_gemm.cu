@@ -11,8 +11,7 @@
 // token whatever d_out is.
 #include <algorithm>
 #include <climits>
-#include <cstdio>
-#include <cstdlib>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -29,9 +28,17 @@ constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;          // warps 0-7: two per tensor-memory lane quarter
 constexpr int kMmaWarp = 8;           // owner of the tensor memory; one thread issues the MMAs
 constexpr int kCopyWarp = 9;          // one thread issues the copies
-constexpr int kThreads = 10 * 32;
+constexpr int kStoreWarp = 10;         // one thread issues the stores of staged outputs
+constexpr int kThreads = 11 * 32;
 
-constexpr uint32_t kRing = 216u * 1024u;  // shared memory of the stages
+// Shared memory of the stages, and of what follows them when outputs are staged:
+// three blocks of 32 tokens x 128 channels of bf16.
+constexpr uint32_t kSmem = 216u * 1024u;
+// Batches up to this size write their outputs directly: too few to fill a block.
+constexpr int kFewTokens = 16;
+constexpr int kBlockTok = 32;             // tokens per staged block of outputs
+constexpr uint32_t kBlock = kBlockTok * kRowsM * 2;
+constexpr int kBlocks = 3;
 constexpr int kMaxSplits = 8;             // CTAs of a cluster
 
 struct Int8GemmArgs {
@@ -47,6 +54,7 @@ struct Int8GemmArgs {
   int tok_tiles;
   int stages;
   int boxes;       // chunks per stage
+  int staged;      // bf16 outputs leave by tensor stores (map_y)
   int splits;      // CTAs (a cluster) that share a tile's chunks; 1: persistent over tiles
 };
 
@@ -107,6 +115,13 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
         "[%1, {%3, %4}], [%2];" ::"r"(dst),
         "l"(map), "r"(bar), "r"(x), "r"(y)
         : "memory");
+}
+
+// Block of shared memory to (column x, row y) of `map`, clipped at its edges.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
 }
 
 // Instruction descriptor of kind::i8: signed A and B (1 at bits 7-9 and 10-12),
@@ -173,6 +188,24 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
                  : "memory");
 }
 
+// 16 lanes x 16 columns of tensor memory as matrix fragments: v[4 j], v[4 j + 1]
+// are columns 8 j + 2 (l % 4), + 1 of lane l / 4 (l: thread of the warp), and
+// v[4 j + 2], v[4 j + 3] those of lane l / 4 + 8.  The caller waits.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, int (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(taddr));
+}
+
+// Four 8 x 8 blocks of 16-bit values, transposed: thread t gives the address of
+// row t % 8 (a column of the fragment) of block t / 8.
+__device__ __forceinline__ void stmatrix4_t(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
 // 16 consecutive 32-bit columns of this warp's 32 tensor-memory lanes.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, int (&v)[16]) {
   asm volatile(
@@ -210,6 +243,7 @@ __device__ __forceinline__ void add_partials(const Int8GemmArgs& a, int64_t i, i
   T* y = reinterpret_cast<T*>(a.y);
   const int nt = min(a.nt, a.ntok - t0), stride = a.splits * kEpiWarps;
   i += 4 * lane;
+  const bool fours = (a.d_out & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7u) == 0;
   float w[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) w[e] = i + e < a.d_out ? __ldg(a.ws + i + e) : 0.f;
@@ -239,10 +273,18 @@ __device__ __forceinline__ void add_partials(const Int8GemmArgs& a, int64_t i, i
         sum[3] += v[j][r].w;
       }
       const float xs = __ldg(a.xs + t0 + c);
+      T* out = y + (int64_t)(t0 + c) * a.d_out + i;
+      float f[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < a.d_out)
-          put(y, (int64_t)(t0 + c) * a.d_out + i + e, __fmul_rn((float)sum[e], __fmul_rn(xs, w[e])));
+      for (int e = 0; e < 4; ++e) f[e] = __fmul_rn((float)sum[e], __fmul_rn(xs, w[e]));
+      if (std::is_same<T, __nv_bfloat16>::value && fours) {
+        if (i < a.d_out)
+          *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < a.d_out) put(out, e, f[e]);
+      }
     }
   }
 }
@@ -260,11 +302,11 @@ __device__ __forceinline__ void add_partials(const Int8GemmArgs& a, int64_t i, i
 template <int CG, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     k_int8_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                const Int8GemmArgs a) {
+                const __grid_constant__ CUtensorMap map_y, const Int8GemmArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], accfull[2], accempty[2], fin;
-  __shared__ __align__(16) float xs_tile[kEpiWarps][256];
+  __shared__ __align__(16) float xs_tile[kEpiWarps][128];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t crank = CG == 2 || a.splits > 1 ? cluster_rank() : 0u;
@@ -389,45 +431,126 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit<CG>(&fin, 1u << leader);
       if (!mbar_wait_bounded(&fin, 0)) flags |= QAMW_STATUS_TIMEOUT;
     }
+  } else if (warp == kStoreWarp) {
+    if (a.staged) {
+      const bool one = elect_one();
+      const uint32_t blocks = smem_u32(smem) + kSmem - kBlocks * kBlock;
+      int block = 0;
+      for (int64_t tile = first; tile < a.tiles; tile += step) {
+        const int64_t m = tile / a.tok_tiles;
+        const int i0 = (int)(m * (kRowsM * CG)) + (int)rank * kRowsM;
+        const int t0 = (int)(tile - m * a.tok_tiles) * a.nt;
+        const int nt = min(a.nt, a.ntok - t0);
+        for (int c = 0; c < nt; c += kBlockTok) {
+          // the block that comes next is free once its stores, the last but one, have
+          // read it: the epilogue warps write it behind this barrier
+          if (one) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+          asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps + 32) : "memory");
+          if (one) {
+            const uint32_t buf = blocks + block * kBlock;
+            if (i0 < a.d_out) store_box(&map_y, i0, t0 + c, buf);
+            if (i0 + 64 < a.d_out) store_box(&map_y, i0 + 64, t0 + c, buf + kBlock / 2);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          block = block == kBlocks - 1 ? 0 : block + 1;
+        }
+      }
+      if (one) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
   } else if (a.splits == 1) {
     T* y = reinterpret_cast<T*>(a.y);
     // warp w: lanes (channels) 32 (w % 4) .. + 31, columns 16 (w / 4) + 32 k .. + 15
     const int q4 = warp & 3, half = warp >> 2;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * q4) << 16);
     float* xs = xs_tile[warp];
-    int n = 0;
+    const uint32_t blocks = smem_u32(smem) + kSmem - kBlocks * kBlock;
+    int n = 0, block = 0;
+    bool alive = true;
     for (int64_t tile = first; tile < a.tiles; tile += step, ++n) {
       const int b = n & 1;
       const int64_t m = tile / a.tok_tiles;
-      const int64_t i = m * (kRowsM * CG) + (CG == 2 ? (int64_t)rank * kRowsM : 0) + 32 * q4 + lane;
+      const int64_t i0 = m * (kRowsM * CG) + (CG == 2 ? (int64_t)rank * kRowsM : 0);
+      const int64_t i = i0 + 32 * q4 + lane;
       const int t0 = (int)(tile - m * a.tok_tiles) * a.nt;
       const int nt = min(a.nt, a.ntok - t0);
       const bool mine = i < a.d_out;
-      const float wi = mine ? __ldg(a.ws + i) : 0.f;
-      for (int c = lane; c < a.nt; c += 32) xs[c] = c < nt ? __ldg(a.xs + t0 + c) : 0.f;
-      // one lane polls: 32 pollers a warp would slow the other roles' waits
-      const bool ok = lane != 0 || mbar_wait_bounded(&accfull[b], (uint32_t)(n >> 1) & 1u);
+      const float wi = !a.staged && mine ? __ldg(a.ws + i) : 0.f;
+      float wg[4];  // staged: channels lane / 4 + 8 g of the warp's 32
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int64_t k = i0 + 32 * q4 + (lane >> 2) + 8 * g;
+        wg[g] = a.staged && k < a.d_out ? __ldg(a.ws + k) : 0.f;
+      }
+      {  // the scales of the warp's tokens, all loads in flight together: entry k is
+         // token 32 (k / 16) + 16 half + k % 16 of the tile
+        float x4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = 64 * k + 32 * (lane >> 4) + 16 * half + (lane & 15);
+          x4[k] = c < nt ? __ldg(a.xs + t0 + c) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) xs[lane + 32 * k] = x4[k];
+        __syncwarp();
+      }
+      // one lane polls: 32 pollers a warp would slow the other roles' waits.  A
+      // wait that gives up is not repeated; the warps still meet at the barriers.
+      const bool ok = !alive || lane != 0 || mbar_wait_bounded(&accfull[b], (uint32_t)(n >> 1) & 1u);
       if (__any_sync(0xffffffffu, !ok)) {
         flags |= QAMW_STATUS_TIMEOUT;
-        break;
+        alive = false;
       }
       tc_fence_after();
-      const int64_t pitch = a.d_out;
-      T* out = y + (t0 + 16 * half) * pitch + i;
-      for (int c = 16 * half; c < nt; c += 32, out += 32 * pitch) {
-        int v[16];
-        tmem_ld16(lane_base + (uint32_t)(b * a.nt + c), v);
-        float f[16];
+      if (a.staged) {
+        // 32 tokens x 128 channels of all eight warps go through shared memory and
+        // leave by tensor stores.  (Direct 2-byte stores, or shuffles to wider ones,
+        // kept the load-store unit busy for 4300 cycles a tile of 256 tokens.)
+        for (int c = 0; c < nt; c += kBlockTok) {
+          const uint32_t buf = blocks + block * kBlock;
+          block = block == kBlocks - 1 ? 0 : block + 1;
+          const int cw = c + 16 * half;
+          if (cw < nt) {
+            int v[2][8];
+            tmem_ld_frag(tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(b * a.nt + cw), v[0]);
+            tmem_ld_frag(tmem + ((uint32_t)(32 * q4 + 16) << 16) + (uint32_t)(b * a.nt + cw), v[1]);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-        for (int e = 0; e < 16; ++e) f[e] = __fmul_rn((float)v[e], __fmul_rn(xs[c + e], wi));
-        if (mine) {
-          if (c + 16 <= nt) {
+            for (int j = 0; j < 2; ++j) {
+              const float2 x2 = *reinterpret_cast<const float2*>(xs + c / 2 + 8 * j + 2 * (lane & 3));
+              uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) put(out, e * pitch, f[e]);
-          } else {
+              for (int g = 0; g < 4; ++g) {
+                const int lo = v[g >> 1][4 * j + 2 * (g & 1)], hi = v[g >> 1][4 * j + 2 * (g & 1) + 1];
+                const float2 f = mul2(make_float2((float)lo, (float)hi), mul2(x2, make_float2(wg[g], wg[g])));
+                w[g] = pack_bf16x2(f.x, f.y);
+              }
+              // block g of eight channels = 16-byte unit 4 (q4 % 2) + g of the 64
+              // channels q4 / 2; swizzled as the tensor store expects
+              const int tok = 16 * half + 8 * j + (lane & 7), unit = 4 * (q4 & 1) + (lane >> 3);
+              stmatrix4_t(buf + (uint32_t)((q4 >> 1) * (kBlock / 2) + tok * 128 + ((unit ^ (tok & 7)) << 4)), w);
+            }
+          }
+          fence_proxy_async_smem();
+          asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps + 32) : "memory");
+        }
+      } else {
+        const int64_t pitch = a.d_out;
+        T* out = y + (t0 + 16 * half) * pitch + i;
+        for (int c = 16 * half; c < nt; c += 32, out += 32 * pitch) {
+          int v[16];
+          tmem_ld16(tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(b * a.nt + c), v);
+          float f[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (c + e < nt) put(out, e * pitch, f[e]);
+          for (int e = 0; e < 16; ++e) f[e] = __fmul_rn((float)v[e], __fmul_rn(xs[c / 32 * 16 + e], wi));
+          if (mine) {
+            if (c + 16 <= nt) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) put(out, e * pitch, f[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (c + e < nt) put(out, e * pitch, f[e]);
+            }
           }
         }
       }
@@ -477,6 +600,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   raise_flag(a.status, flags);
 }
 
+// bf16 [rows][d_out] for tensor stores of 64 channels (one swizzled line) x 32 tokens.
+bool encode_out_map(CUtensorMap* map, void* p, int64_t rows, int d_out) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)d_out, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d_out * 2};
+  const cuuint32_t boxes[2] = {64, kBlockTok};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, boxes, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 8-bit matrix [rows][d_in] for boxes of 128 bytes x `box` rows, swizzled.
 bool encode_map(CUtensorMap* map, const int8_t* p, int64_t rows, int d_in, int box) {
   const auto enc = tensor_map_encoder();
@@ -492,11 +628,12 @@ bool encode_map(CUtensorMap* map, const int8_t* p, int64_t rows, int d_in, int b
 
 struct Int8Plan {
   int cg, nt, splits, boxes, stages;
+  bool staged;
 };
 
-// Estimated time (ns) of a plan, fitted to 350 measured (shape, plan) pairs from
-// 1 x 512 -> 1000 to 3000 x 4096 -> 11008; over those 24 shapes the plan that it
-// picks is within 3% of the fastest one measured.  A chunk of a CTA costs the
+// Estimated time (ns) of a plan, fitted to 360 measured (shape, plan) pairs from
+// 1 x 512 -> 1000 to 3000 x 4096 -> 11008; over those 26 shapes the plan that it
+// picks is within 5% of the fastest one measured (mean 0.4%).  A chunk of a CTA costs the
 // longest of its MMAs, its way through shared memory (128 channels and nt / cg
 // tokens) and a floor; the last tile's epilogue is not hidden, earlier ones are
 // unless the depth is short; sharing a tile's chunks among CTAs costs two
@@ -506,14 +643,15 @@ int plan_ns(int ntok, int d_out, int chunks, int cg, int nt, int splits, int sms
       (int64_t)((d_out + kRowsM * cg - 1) / (kRowsM * cg)) * ((ntok + nt - 1) / nt);
   const int at_once = std::max(1, sms / (cg * splits));
   const int64_t waves = (tiles + at_once - 1) / at_once;
-  const int chunk = std::max(std::max(118 * nt / 100, 87 * (kRowsM + nt / cg) / 100), 197);
-  const int main = (chunks + splits - 1) / splits * chunk, epilogue = 11 * nt;
-  int64_t t = waves * (std::max(main, epilogue) + 1500) + epilogue;
-  if (splits > 1) t += waves * 4300 + (waves - 1) * epilogue + 7 * nt;
+  const int chunk = std::max(std::max(135 * nt / 100, 98 * (kRowsM + nt / cg) / 100), 227);
+  const int main = (chunks + splits - 1) / splits * chunk, epilogue = 10 * nt;
+  int64_t t = waves * (std::max(main, epilogue) + 1270) + epilogue;
+  if (splits > 1) t += waves * 5200 + (waves - 1) * epilogue + 2 * nt;
   return (int)std::min<int64_t>(t, INT_MAX);
 }
 
-Int8Plan plan_int8(int ntok, int d_out, int d_in) {
+// bf16_rows: bf16 outputs whose rows are multiples of 16 bytes.
+Int8Plan plan_int8(int ntok, int d_out, int d_in, bool bf16_rows) {
   Int8Plan p = {};
   const int chunks = (d_in + kChunk - 1) / kChunk, sms = sm_count();
   int best = INT_MAX;
@@ -535,25 +673,24 @@ Int8Plan plan_int8(int ntok, int d_out, int d_in) {
         }
       }
   }
-  int ovb = 0, ovr = 0; if (const char* e = getenv("QI8")) sscanf(e, "%d,%d,%d,%d,%d", &p.cg, &p.nt, &p.splits, &ovb, &ovr);
   // the wait for a stage and its commit cost the MMA thread about 240 cycles:
   // several chunks per stage, as long as three stages fit
-  const uint32_t ring = kRing;
+  p.staged = bf16_rows && p.splits == 1 && ntok > kFewTokens && (p.nt % kBlockTok == 0 || ntok <= p.nt);
+  const uint32_t ring = kSmem - (p.staged ? kBlocks * kBlock : 0);
   p.boxes = 4;
-  while (p.boxes > 1 && ring / (box_bytes(p.cg, p.nt) * p.boxes) < 3) p.boxes /= 2;
-  if (ovb) p.boxes = ovb;
+  while (p.boxes > 1 && ring / (box_bytes(p.cg, p.nt) * p.boxes) < 3) --p.boxes;
   p.stages = (int)std::min<uint32_t>(kMaxStages, ring / (box_bytes(p.cg, p.nt) * p.boxes));
   return p;
 }
 
 template <int CG, typename T>
 cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap& mx,
-                     const Int8GemmArgs& a, cudaStream_t stream) {
+                     const CUtensorMap& my, const Int8GemmArgs& a, cudaStream_t stream) {
   auto fn = &k_int8_gemm<CG, T>;
   // all of the ring, whatever the stages need of it: one CTA that owns tensor
   // memory per SM, so that an allocation never waits for a CTA that could be
   // waiting for it
-  constexpr size_t smem = kRing + 1024;
+  constexpr size_t smem = kSmem + 1024;
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(fn), smem);
   if (err != cudaSuccess) return err;
   const int per = CG * p.splits;
@@ -572,7 +709,7 @@ cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = per > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fn, mw, mx, a);
+  return cudaLaunchKernelEx(&cfg, fn, mw, mx, my, a);
 }
 
 }  // namespace
@@ -580,8 +717,10 @@ cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap
 cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
                              int32_t* d_status, cudaStream_t stream) {
-  const Int8Plan p = plan_int8(ntok, d_out, d_in);
-  CUtensorMap mw, mx;
+  const Int8Plan p = plan_int8(ntok, d_out, d_in,
+                               dtype == QAMW_DTYPE_BF16 && d_out % 8 == 0 &&
+                                   (reinterpret_cast<uintptr_t>(d_y) & 15u) == 0);
+  CUtensorMap mw, mx, my = {};
   if (!encode_map(&mw, d_w, d_out, d_in, kRowsM) || !encode_map(&mx, d_x, ntok, d_in, p.nt / p.cg))
     return cudaErrorInvalidValue;
   Int8GemmArgs a = {};
@@ -599,11 +738,13 @@ cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok
   a.stages = p.stages;
   a.boxes = p.boxes;
   a.splits = p.splits;
+  a.staged = p.staged;
+  if (a.staged && !encode_out_map(&my, d_y, ntok, d_out)) return cudaErrorInvalidValue;
   if (dtype == QAMW_DTYPE_F32)
-    return p.cg == 2 ? run_gemm<2, float>(p, mw, mx, a, stream)
-                     : run_gemm<1, float>(p, mw, mx, a, stream);
-  return p.cg == 2 ? run_gemm<2, __nv_bfloat16>(p, mw, mx, a, stream)
-                   : run_gemm<1, __nv_bfloat16>(p, mw, mx, a, stream);
+    return p.cg == 2 ? run_gemm<2, float>(p, mw, mx, my, a, stream)
+                     : run_gemm<1, float>(p, mw, mx, my, a, stream);
+  return p.cg == 2 ? run_gemm<2, __nv_bfloat16>(p, mw, mx, my, a, stream)
+                   : run_gemm<1, __nv_bfloat16>(p, mw, mx, my, a, stream);
 }
 
 }  // namespace qamw
