@@ -545,25 +545,38 @@ def _status_ptr(status: torch.Tensor | None, index: int):
     return None if status is None else _dense("status", status, torch.int32, status.shape, index)
 
 
-def _int8_encode(fn: str, what: str, x, chan_scale, q, scale, status, stream):
+def _new_codes(x, q, scale):
+    """The 8-bit codes of the rows of x and their scales: the given tensors, checked, or new ones,
+    and the addresses of both."""
+    rows, d = x.shape
+    dev = x.get_device()
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.int8)
+        qp = q.data_ptr()
+    else:
+        qp = _dense("q", q, torch.int8, (rows, d), dev)
+    if scale is None:
+        scale = x.new_empty(rows, dtype=torch.float32)
+        sp = scale.data_ptr()
+    else:
+        sp = _dense("scale", scale, torch.float32, (rows,), dev)
+    return q, scale, qp, sp
+
+
+def _int8_encode(fn, what: str, x, chan_scale, q, scale, status, stream):
     code = _rows_of(what, x)
     rows, d = x.shape
     dev = x.get_device()
+    sp = None if chan_scale is None else _dense("chan_scale", chan_scale, torch.float16, (d,), dev)
     ctx = _enter(dev, stream)
     try:
-        if q is None:
-            q = torch.empty_like(x, dtype=torch.int8)
-        if scale is None:
-            scale = x.new_empty(rows, dtype=torch.float32)
-        _check(fn, getattr(_lib, fn)(
-            x.data_ptr(), code, rows, d,
-            None if chan_scale is None else _dense("chan_scale", chan_scale, torch.float16, (d,), dev),
-            _dense("q", q, torch.int8, (rows, d), dev),
-            _dense("scale", scale, torch.float32, (rows,), dev), _status_ptr(status, dev),
-            _raw_stream(dev)))
+        q, scale, qp, scp = _new_codes(x, q, scale)
+        rc = fn(x.data_ptr(), code, rows, d, sp, qp, scp, _status_ptr(status, dev), _raw_stream(dev))
     finally:
         if ctx is not None:
             ctx.close()
+    if rc != QAMW_OK:
+        raise QamwError(fn.__name__, rc)
     return q, scale
 
 
@@ -572,7 +585,7 @@ def qamw_int8_encode_weights(W: torch.Tensor, chan_scale: torch.Tensor | None = 
                              status: torch.Tensor | None = None, stream=None):
     """W * chan_scale (W: bf16 or float32 [d_out, d_in], chan_scale: binary16 [d_in]) as int8
     [d_out, d_in] with one float32 scale per row; returns (q, row_scale)."""
-    return _int8_encode("qamw_int8_encode_weights", "W", W, chan_scale, q, row_scale, status, stream)
+    return _int8_encode(_lib.qamw_int8_encode_weights, "W", W, chan_scale, q, row_scale, status, stream)
 
 
 def qamw_int8_encode_tokens(x: torch.Tensor, chan_scale: torch.Tensor | None = None,
@@ -580,7 +593,7 @@ def qamw_int8_encode_tokens(x: torch.Tensor, chan_scale: torch.Tensor | None = N
                             status: torch.Tensor | None = None, stream=None):
     """x / chan_scale (x: bf16 or float32 [ntok, d]) as int8 [ntok, d] with one float32 scale
     per token; returns (q, tok_scale)."""
-    return _int8_encode("qamw_int8_encode_tokens", "x", x, chan_scale, q, tok_scale, status, stream)
+    return _int8_encode(_lib.qamw_int8_encode_tokens, "x", x, chan_scale, q, tok_scale, status, stream)
 
 
 def qamw_rmsnorm_int8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-5,
@@ -596,26 +609,22 @@ def qamw_rmsnorm_int8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-5,
     dev = x.get_device()
     if residual is None and sum_out is not None:
         raise ValueError("sum_out needs a residual")
+    gp = _dense("gain", gain, x.dtype, (d,), dev)
+    cp = None if chan_scale is None else _dense("chan_scale", chan_scale, torch.float16, (d,), dev)
+    rp = None if residual is None else _dense("residual", residual, x.dtype, (rows, d), dev)
+    hp = None if sum_out is None else _dense("sum_out", sum_out, x.dtype, (rows, d), dev)
     ctx = _enter(dev, stream)
     try:
         if residual is not None and sum_out is None:
             sum_out = torch.empty_like(x)
-        if q is None:
-            q = torch.empty_like(x, dtype=torch.int8)
-        if tok_scale is None:
-            tok_scale = x.new_empty(rows, dtype=torch.float32)
-        _check("qamw_rmsnorm_int8", _lib.qamw_rmsnorm_int8(
-            x.data_ptr(),
-            None if residual is None else _dense("residual", residual, x.dtype, (rows, d), dev),
-            code, _dense("gain", gain, x.dtype, (d,), dev), eps, rows, d,
-            None if chan_scale is None else _dense("chan_scale", chan_scale, torch.float16, (d,), dev),
-            None if residual is None else _dense("sum_out", sum_out, x.dtype, (rows, d), dev),
-            _dense("q", q, torch.int8, (rows, d), dev),
-            _dense("tok_scale", tok_scale, torch.float32, (rows,), dev),
-            _status_ptr(status, dev), _raw_stream(dev)))
+            hp = sum_out.data_ptr()
+        q, tok_scale, qp, sp = _new_codes(x, q, tok_scale)
+        rc = _lib.qamw_rmsnorm_int8(x.data_ptr(), rp, code, gp, eps, rows, d, cp, hp, qp, sp,
+                                    _status_ptr(status, dev), _raw_stream(dev))
     finally:
         if ctx is not None:
             ctx.close()
+    _check("qamw_rmsnorm_int8", rc)
     return (q, tok_scale) if residual is None else (sum_out, q, tok_scale)
 
 
@@ -634,18 +643,21 @@ def qamw_int8_gemm(xq: torch.Tensor, tok_scale: torch.Tensor, wq: torch.Tensor,
     code = _DTYPE_CODE.get(dtype)
     if code is None:
         raise ValueError(f"y must be float32 or bfloat16, not {dtype}")
+    xp = _dense("xq", xq, torch.int8, (ntok, d_in), dev)
+    sp = _dense("tok_scale", tok_scale, torch.float32, (ntok,), dev)
+    wp = _dense("wq", wq, torch.int8, (d_out, d_in), dev)
+    rp = _dense("row_scale", row_scale, torch.float32, (d_out,), dev)
     ctx = _enter(dev, stream)
     try:
         if y is None:
             y = xq.new_empty((ntok, d_out), dtype=dtype)
-        _check("qamw_int8_gemm", _lib.qamw_int8_gemm(
-            _dense("xq", xq, torch.int8, (ntok, d_in), dev),
-            _dense("tok_scale", tok_scale, torch.float32, (ntok,), dev), ntok,
-            _dense("wq", wq, torch.int8, (d_out, d_in), dev),
-            _dense("row_scale", row_scale, torch.float32, (d_out,), dev), d_out, d_in,
-            _dense("y", y, dtype, (ntok, d_out), dev), code, _status_ptr(status, dev),
-            _raw_stream(dev)))
+            yp = y.data_ptr()
+        else:
+            yp = _dense("y", y, dtype, (ntok, d_out), dev)
+        rc = _lib.qamw_int8_gemm(xp, sp, ntok, wp, rp, d_out, d_in, yp, code,
+                                 _status_ptr(status, dev), _raw_stream(dev))
     finally:
         if ctx is not None:
             ctx.close()
+    _check("qamw_int8_gemm", rc)
     return y
