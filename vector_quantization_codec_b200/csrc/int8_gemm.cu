@@ -232,51 +232,50 @@ __host__ __device__ inline uint32_t tmem_cols(int nt) {
 
 // Sum of the `splits` partial tiles [token][128 channels] of a cluster: CTA
 // `split` adds up and writes tokens split, split + splits, ..., of its 128
-// channels, a warp one token at a time, a lane four channels; the loads of two
-// tokens from all CTAs are in flight together.  The CTAs with the same channels
-// have the cluster ranks r0, r0 + CG, ...
+// channels, a warp one token at a time (its k-th is split + splits (warp + 8 k)),
+// a lane four channels i, i + 1, ...; 16 loads in flight.  The CTAs with the same
+// channels have the cluster ranks r0, r0 + CG, ...; w and xs are the scales of
+// the lane's channels and of the warp's tokens, loaded long before.
 template <int CG, typename T>
 __device__ __forceinline__ void add_partials(const Int8GemmArgs& a, int64_t i, int t0, int split,
-                                             uint32_t r0, uint32_t part, int warp, int lane) {
-  constexpr int kAhead = 2;
-  constexpr int kMost = kMaxSplits / CG;
+                                             uint32_t r0, uint32_t part, int warp, int lane,
+                                             const float (&w)[4], const float* xs) {
+  constexpr int kAhead = 4, kRanks = 4;
   T* y = reinterpret_cast<T*>(a.y);
-  const int nt = min(a.nt, a.ntok - t0), stride = a.splits * kEpiWarps;
-  i += 4 * lane;
   const bool fours = (a.d_out & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7u) == 0;
-  float w[4];
+  const int nt = min(a.nt, a.ntok - t0), c0 = split + a.splits * warp, stride = a.splits * kEpiWarps;
+  for (int k0 = 0; c0 + k0 * stride < nt; k0 += kAhead) {
+    int sum[kAhead][4] = {};
+    for (int rb = 0; rb < a.splits; rb += kRanks) {
+      int4 v[kAhead][kRanks];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = i + e < a.d_out ? __ldg(a.ws + i + e) : 0.f;
-  uint32_t from[kMost];
+      for (int r = 0; r < kRanks; ++r) {
+        const uint32_t from = cluster_addr(part + 16u * lane, r0 + (uint32_t)(CG * min(rb + r, a.splits - 1)));
 #pragma unroll
-  for (int r = 0; r < kMost; ++r)
-    from[r] = cluster_addr(part + 16u * lane, r0 + (uint32_t)(CG * min(r, a.splits - 1)));
-  for (int c0 = split + a.splits * warp; c0 < nt; c0 += stride * kAhead) {
-    int4 v[kAhead][kMost];
+        for (int j = 0; j < kAhead; ++j) {
+          const int c = c0 + (k0 + j) * stride;
+          v[j][r] = rb + r < a.splits && c < nt ? lds_cluster(from + 4u * kRowsM * (uint32_t)c)
+                                                : make_int4(0, 0, 0, 0);
+        }
+      }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const uint32_t at = 4u * kRowsM * (uint32_t)min(c0 + j * stride, a.nt - 1);
+      for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-      for (int r = 0; r < kMost; ++r)
-        v[j][r] = r < a.splits ? lds_cluster(from[r] + at) : make_int4(0, 0, 0, 0);
+        for (int r = 0; r < kRanks; ++r) {
+          sum[j][0] += v[j][r].x;
+          sum[j][1] += v[j][r].y;
+          sum[j][2] += v[j][r].z;
+          sum[j][3] += v[j][r].w;
+        }
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int c = c0 + j * stride;
+      const int c = c0 + (k0 + j) * stride;
       if (c >= nt) break;
-      int sum[4] = {};
-#pragma unroll
-      for (int r = 0; r < kMost; ++r) {
-        sum[0] += v[j][r].x;
-        sum[1] += v[j][r].y;
-        sum[2] += v[j][r].z;
-        sum[3] += v[j][r].w;
-      }
-      const float xs = __ldg(a.xs + t0 + c);
       T* out = y + (int64_t)(t0 + c) * a.d_out + i;
       float f[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = __fmul_rn((float)sum[e], __fmul_rn(xs, w[e]));
+      for (int e = 0; e < 4; ++e) f[e] = __fmul_rn((float)sum[j][e], __fmul_rn(xs[k0 + j], w[e]));
       if (std::is_same<T, __nv_bfloat16>::value && fours) {
         if (i < a.d_out)
           *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
@@ -346,6 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
   int flags = 0;
+  int64_t split_i = 0;
+  int split_t0 = 0;
+  float split_w[4] = {};
 
   if (warp == kCopyWarp) {
     if (elect_one()) {
@@ -564,6 +566,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
+    // the scales that add_partials will need, while the products come in
+    const int64_t m = first / a.tok_tiles;
+    split_i = m * (kRowsM * CG) + (int64_t)rank * kRowsM + 4 * lane;
+    split_t0 = (int)(first - m * a.tok_tiles) * a.nt;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_w[e] = split_i + e < a.d_out ? __ldg(a.ws + split_i + e) : 0.f;
+    {
+      const int t = split_t0 + split + a.splits * (warp + kEpiWarps * lane);
+      xs_tile[warp][lane] = t < a.ntok ? __ldg(a.xs + t) : 0.f;
+    }
     // the CTA's partial sums into its own shared memory (the stages are free:
     // every MMA that reads them is done), [token][channel]
     int* part = reinterpret_cast<int*>(smem);
@@ -581,12 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.splits > 1) {
     __syncwarp();
     cluster_sync();
-    if (warp < kEpiWarps) {
-      const int64_t m = first / a.tok_tiles;
-      add_partials<CG, T>(a, m * (kRowsM * CG) + (int64_t)rank * kRowsM,
-                          (int)(first - m * a.tok_tiles) * a.nt, split, rank, smem_u32(smem), warp,
-                          lane);
-    }
+    if (warp < kEpiWarps)
+      add_partials<CG, T>(a, split_i, split_t0, split, rank, smem_u32(smem), warp, lane, split_w,
+                          xs_tile[warp]);
   }
   __syncwarp();
   if (CG == 2 || a.splits > 1)
