@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  // every operand and scale may come from the kernel ahead
+  // every operand and scale may come from the kernel ahead (which is why the scales
+  // are not read through the read-only path)
   pdl_wait();
   pdl_trigger();
   int flags = 0;
@@ -351,9 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kCopyWarp) {
     if (elect_one()) {
+      // what the kernel ahead wrote is read by asynchronous copies from here on
+      asm volatile("fence.proxy.async.global;" ::: "memory");
       int s = 0;
       uint32_t u = 0;
-      int64_t issued = 0;
       bool ok = true;
       for (int64_t tile = first; tile < a.tiles && ok; tile += step) {
         const int64_t m = tile / a.tok_tiles;
@@ -372,23 +374,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             copy_box<CG>(dst, &map_w, (c + j) * kChunk, row, bar);
             copy_box<CG>(dst + kTileA, &map_x, (c + j) * kChunk, tok, bar);
           }
-          ++issued;
           if (++s == S) {
             s = 0;
             ++u;
           }
         }
       }
-      // nothing in flight at exit: the last use of each stage has been consumed
-      // (which also means that a pair's arrivals on these barriers have landed)
-      const int64_t last = issued > S ? issued - S : 0;
-      for (int64_t j = last; j < issued && ok; ++j)
-        ok = mbar_wait_bounded(&empty[j % S], (uint32_t)(j / S) & 1u);
+      // nothing in flight at exit: the last use of each stage (in round u, or u - 1 from
+      // stage s on) has been consumed, which also means that a pair's arrivals on these
+      // barriers have landed
+      const int used = u > 0 ? S : s;
+      for (int k = 0; k < used && ok; ++k)
+        ok = mbar_wait_bounded(&empty[k], (k < s ? u : u - 1) & 1u);
       if (!ok) {  // given up: the copies at least have to land (a pair's leader waits for both)
         flags |= QAMW_STATUS_TIMEOUT;
         if (CG == 1 || rank == 0)
-          for (int64_t j = last; j < issued; ++j)
-            if (!mbar_wait_bounded(&full[j % S], (uint32_t)(j / S) & 1u)) break;
+          for (int k = 0; k < used; ++k)
+            if (!mbar_wait_bounded(&full[k], (k < s ? u : u - 1) & 1u)) break;
       }
     }
   } else if (warp == kMmaWarp) {
@@ -476,12 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t0 = (int)(tile - m * a.tok_tiles) * a.nt;
       const int nt = min(a.nt, a.ntok - t0);
       const bool mine = i < a.d_out;
-      const float wi = !a.staged && mine ? __ldg(a.ws + i) : 0.f;
+      const float wi = !a.staged && mine ? a.ws[i] : 0.f;
       float wg[4];  // staged: channels lane / 4 + 8 g of the warp's 32
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int64_t k = i0 + 32 * q4 + (lane >> 2) + 8 * g;
-        wg[g] = a.staged && k < a.d_out ? __ldg(a.ws + k) : 0.f;
+        wg[g] = a.staged && k < a.d_out ? a.ws[k] : 0.f;
       }
       {  // the scales of the warp's tokens, all loads in flight together: entry k is
          // token 32 (k / 16) + 16 half + k % 16 of the tile
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = 64 * k + 32 * (lane >> 4) + 16 * half + (lane & 15);
-          x4[k] = c < nt ? __ldg(a.xs + t0 + c) : 0.f;
+          x4[k] = c < nt ? a.xs[t0 + c] : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) xs[lane + 32 * k] = x4[k];
@@ -571,10 +573,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     split_i = m * (kRowsM * CG) + (int64_t)rank * kRowsM + 4 * lane;
     split_t0 = (int)(first - m * a.tok_tiles) * a.nt;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) split_w[e] = split_i + e < a.d_out ? __ldg(a.ws + split_i + e) : 0.f;
+    for (int e = 0; e < 4; ++e) split_w[e] = split_i + e < a.d_out ? a.ws[split_i + e] : 0.f;
     {
       const int t = split_t0 + split + a.splits * (warp + kEpiWarps * lane);
-      xs_tile[warp][lane] = t < a.ntok ? __ldg(a.xs + t) : 0.f;
+      xs_tile[warp][lane] = t < a.ntok ? a.xs[t] : 0.f;
     }
     // the CTA's partial sums into its own shared memory (the stages are free:
     // every MMA that reads them is done), [token][channel]
@@ -642,7 +644,7 @@ struct Int8Plan {
 
 // Estimated time (ns) of a plan, fitted to 360 measured (shape, plan) pairs from
 // 1 x 512 -> 1000 to 3000 x 4096 -> 11008; over those 26 shapes the plan that it
-// picks is within 5% of the fastest one measured (mean 0.4%).  A chunk of a CTA costs the
+// picks is within 4% of the fastest one measured (mean 0.3%).  A chunk of a CTA costs the
 // longest of its MMAs, its way through shared memory (128 channels and nt / cg
 // tokens) and a floor; the last tile's epilogue is not hidden, earlier ones are
 // unless the depth is short; sharing a tile's chunks among CTAs costs two
@@ -652,10 +654,10 @@ int plan_ns(int ntok, int d_out, int chunks, int cg, int nt, int splits, int sms
       (int64_t)((d_out + kRowsM * cg - 1) / (kRowsM * cg)) * ((ntok + nt - 1) / nt);
   const int at_once = std::max(1, sms / (cg * splits));
   const int64_t waves = (tiles + at_once - 1) / at_once;
-  const int chunk = std::max(std::max(135 * nt / 100, 98 * (kRowsM + nt / cg) / 100), 227);
+  const int chunk = std::max(std::max(118 * nt / 100, 98 * (kRowsM + nt / cg) / 100), 225);
   const int main = (chunks + splits - 1) / splits * chunk, epilogue = 10 * nt;
-  int64_t t = waves * (std::max(main, epilogue) + 1270) + epilogue;
-  if (splits > 1) t += waves * 5200 + (waves - 1) * epilogue + 2 * nt;
+  int64_t t = waves * (std::max(main, epilogue) + 1900) + epilogue;
+  if (splits > 1) t += waves * 2150 + (waves - 1) * epilogue + 7 * nt;
   return (int)std::min<int64_t>(t, INT_MAX);
 }
 

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32, 4) k_int8_gemv(const Int8Gemv
   int64_t r = (int64_t)blockIdx.x * rows_cta + mine * ROWS;  // this warp's first row
   load(r, g * 32 + lane);                                    // in flight while the tokens come in
   for (int v = threadIdx.x; v < NTOK * nv; v += kGemvWarps * 32)
-    xv[v] = v < a.ntok * nv ? __ldg(reinterpret_cast<const uint4*>(a.x) + v) : make_uint4(0u, 0u, 0u, 0u);
+    xv[v] = v < a.ntok * nv ? reinterpret_cast<const uint4*>(a.x)[v] : make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
   int parity = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * rows_cta; r0 < a.d_out; r0 += step, r += step) {
@@ -115,12 +115,12 @@ __global__ void __launch_bounds__(kGemvWarps * 32, 4) k_int8_gemv(const Int8Gemv
 #pragma unroll
       for (int k = 0; k < ROWS; ++k)
         if (r + k < a.d_out) {
-          const float wi = __ldg(a.ws + r + k);
+          const float wi = a.ws[r + k];
 #pragma unroll
           for (int t = 0; t < NTOK; ++t)
             if (t < a.ntok)
               put(y + (int64_t)t * a.d_out + r + k,
-                  __fmul_rn((float)acc[k][t], __fmul_rn(__ldg(a.xs + t), wi)));
+                  __fmul_rn((float)acc[k][t], __fmul_rn(a.xs[t], wi)));
         }
     }
   }

@@ -117,8 +117,17 @@ __device__ __forceinline__ void factors(const Int8RowsArgs& a, int vec, float2 (
     for (int i = 0; i < 4; ++i) c[i] = make_float2(1.f, 1.f);
   }
   if (a.s != nullptr) {
+    // from L2, not by the read-only path: the kernel ahead, which may have written s,
+    // was still running when this one began
+    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(a.s) + vec);
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
     float s[8];
-    load_halves<8>(a.s + 8 * vec, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(h[i]);
+      s[2 * i] = f.x;
+      s[2 * i + 1] = f.y;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       c[i] = a.divide ? make_float2(__fdiv_rn(c[i].x, s[2 * i]), __fdiv_rn(c[i].y, s[2 * i + 1]))
@@ -385,12 +394,14 @@ __global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
     k_int8_ring(const Int8RowsArgs a, int stages) {
   __shared__ RowSlots slots[2];
   __shared__ uint64_t full[kRingMax];
+  __shared__ int gave_up;
   extern __shared__ __align__(128) unsigned char ring[];
   const int n = blockDim.x - 32, t = threadIdx.x, nvec = a.d / 8;
   const int lane = t & 31, warp = t >> 5, nwarps = n >> 5;
   const uint32_t row_bytes = (uint32_t)a.d * sizeof(T), stage = row_bytes * (RES ? 2 : 1);
   if (t == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    gave_up = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -419,6 +430,11 @@ __global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
       parity ^= 1;
       if (++s == stages) s = 0;
     }
+    if (gave_up) {  // no copy in flight at exit, here too
+      const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+      for (int64_t j = mine > stages ? mine - stages : 0; j < mine; ++j)
+        if (!mbar_wait_bounded(&full[j % stages], (uint32_t)(j / stages) & 1u)) break;
+    }
   } else {
     float2 c[kRingVec][4];
 #pragma unroll
@@ -431,6 +447,7 @@ __global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
       // a wait that gives up is not repeated; the row's barriers are still met
       if (alive && !mbar_wait_bounded(&full[s], u & 1u)) {
         alive = false;
+        gave_up = 1;
         flags |= QAMW_STATUS_TIMEOUT;
       }
       const unsigned char* src = ring + (size_t)s * stage;

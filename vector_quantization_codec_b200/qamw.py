@@ -519,7 +519,8 @@ def _rows_of(name: str, x: torch.Tensor) -> int:
 
 
 # The current stream's handle without building a Stream object (a few microseconds a call).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _enter(index: int, stream):
