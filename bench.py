@@ -976,6 +976,87 @@ def run_reference(args) -> dict | None:
 
 # ------------------------------------------------------------------ profiling
 
+def time_stage(fn, args) -> float:
+    """Milliseconds per call of `fn`: `warmup` untimed calls, then `steps` timed ones,
+    eager or as one CUDA graph of back-to-back calls (device time only)."""
+    import torch
+    for _ in range(args.warmup):
+        fn()
+    torch.cuda.synchronize()
+    e0 = torch.cuda.Event(enable_timing=True)
+    e1 = torch.cuda.Event(enable_timing=True)
+    if args.eager:
+        e0.record()
+        for _ in range(args.steps):
+            fn()
+        e1.record()
+    else:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(args.steps):
+                fn()
+        graph.replay()
+        torch.cuda.synchronize()
+        e0.record()
+        graph.replay()
+        e1.record()
+    torch.cuda.synchronize()
+    return e0.elapsed_time(e1) / args.steps
+
+
+INT8_STAGES = ("int8_encode", "int8_norm", "int8_gemm")
+
+
+def run_int8_stage(args) -> dict:
+    """One 8-bit (W8A8) stage alone: encoding a rows x din weight matrix, the residual norm of
+    `batch` tokens of din channels, or the product of the two, over three sets of inputs in
+    turn."""
+    import itertools
+
+    import torch
+
+    from vector_quantization_codec_b200 import qamw, synth
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    rows, d_in, batch = args.rows, args.din, args.batch
+    act = torch.from_numpy(synth.act_stat_lognormal(d_in, args.seed)).to(dev)
+    s = qamw.qamw_channel_scales(d_in, act, ALPHA, torch.empty(d_in, dtype=torch.float16, device=dev))
+    gain = torch.ones(d_in, dtype=torch.bfloat16, device=dev)
+    sets = []
+    for k in range(3):
+        W = synth.student_t_weights_device(rows, d_in, (9, args.seed, k), dev)
+        x = torch.from_numpy(synth.gemv_x(batch, d_in, args.seed + k)).to(torch.bfloat16).to(dev)
+        res = x.flip(0).contiguous() + 1
+        h, xq, xs = qamw.qamw_rmsnorm_int8(x, gain, residual=res, chan_scale=s)
+        wq, ws = qamw.qamw_int8_encode_weights(W, s)
+        y = torch.empty((batch, rows), dtype=torch.bfloat16, device=dev)
+        sets.append((W, x, res, h, xq, xs, wq, ws, y))
+    turn = itertools.cycle(sets)
+
+    def encode():
+        W, _, _, _, _, _, wq, ws, _ = next(turn)
+        qamw.qamw_int8_encode_weights(W, s, wq, ws)
+
+    def norm():
+        _, x, res, h, xq, xs, _, _, _ = next(turn)
+        qamw.qamw_rmsnorm_int8(x, gain, residual=res, chan_scale=s, sum_out=h, q=xq, tok_scale=xs)
+
+    def gemm():
+        _, _, _, _, xq, xs, wq, ws, y = next(turn)
+        qamw.qamw_int8_gemm(xq, xs, wq, ws, y=y)
+
+    ms = time_stage(dict(zip(INT8_STAGES, (encode, norm, gemm)))[args.only], args)
+    nbytes = {"int8_encode": 3 * rows * d_in + 4 * rows + 2 * d_in,
+              "int8_norm": 7 * batch * d_in + 4 * batch + 4 * d_in,
+              "int8_gemm": (rows + batch) * d_in + 4 * (rows + batch) + 2 * rows * batch}[args.only]
+    out = dict(stage=args.only, rows=rows, d_in=d_in, batch=batch, ms=ms,
+               timing="eager" if args.eager else "cuda graph of back-to-back calls",
+               GB_per_s=nbytes / (ms * 1e-3) / 1e9)
+    if args.only == "int8_gemm":
+        out["TOP_per_s"] = 2 * rows * batch * d_in / (ms * 1e-3) / 1e12
+    return out
+
+
 def run_single_stage(args) -> dict:
     """One stage alone on a d_out = args.rows x args.din matrix (same
     distributions), for kernel profiling and sweeps: `warmup` untimed then
@@ -1035,30 +1116,7 @@ def run_single_stage(args) -> dict:
                                                            workspace=ws_cm),
         "train": lambda: qamw.qamw_train_codebook(samples, bits, 1, codebook),
     }
-    fn = fns[args.only]
-    for _ in range(args.warmup):
-        fn()
-    torch.cuda.synchronize()
-    e0 = torch.cuda.Event(enable_timing=True)
-    e1 = torch.cuda.Event(enable_timing=True)
-    if args.eager:
-        e0.record()
-        for _ in range(args.steps):
-            fn()
-        e1.record()
-    else:
-        # `steps` back-to-back calls captured in one CUDA graph: device time only
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
-            for _ in range(args.steps):
-                fn()
-        graph.replay()
-        torch.cuda.synchronize()
-        e0.record()
-        graph.replay()
-        e1.record()
-    torch.cuda.synchronize()
-    ms = e0.elapsed_time(e1) / args.steps
+    ms = time_stage(fns[args.only], args)
     ab = algorithmic_bytes(rows, d_in, bits, args.batch)
     key = {"encode": "encode", "calibrate": "encode", "decode": "decode", "gemv": "gemv",
            "gemm": "gemv", "gemv_many": "gemv"}.get(args.only)
@@ -1090,12 +1148,12 @@ def main(argv=None) -> int:
                     help="--impl reference: rows of each sample step")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--only", choices=["encode", "calibrate", "calibrate_many", "decode", "gemv",
-                                       "gemv_many", "gemm", "train"],
+                                       "gemv_many", "gemm", "train", *INT8_STAGES],
                     help="profiling mode: time one stage alone (no step, no JSON contract)")
     ap.add_argument("--rows", type=int, default=16384, help="--only: rows of the matrix")
     ap.add_argument("--din", type=int, default=4096, help="--only: columns of the matrix")
     ap.add_argument("--bits", type=int, default=BITS, help="--only: bits per pair")
-    ap.add_argument("--batch", type=int, default=1, help="--only gemv / gemm: batch columns / tokens")
+    ap.add_argument("--batch", type=int, default=1, help="--only gemv / gemm / int8_*: batch columns / tokens")
     ap.add_argument("--count", type=int, default=16,
                     help="--only gemv_many / calibrate_many: matrices in the list")
     ap.add_argument("--seed", type=int, default=0)
@@ -1104,7 +1162,8 @@ def main(argv=None) -> int:
     if args.warmup < 3:
         ap.error("--warmup must be at least 3")
     if args.only:
-        print(json.dumps(run_single_stage(args)), flush=True)
+        stage = run_int8_stage if args.only in INT8_STAGES else run_single_stage
+        print(json.dumps(stage(args)), flush=True)
         return 0
     out = run_reference(args) if args.impl == "reference" else run_gpu(args)
     if out is not None:

@@ -482,3 +482,14 @@ def test_product_feeds_the_decode_products():
             q, _ = qamw.qamw_int8_encode_tokens(got.repeat(1, 2)[:, :128].contiguous())
             torch.cuda.synchronize()
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("stage", ["int8_encode", "int8_norm", "int8_gemm"])
+def test_benchmark_stage(stage, capsys):
+    import json
+
+    import bench
+    assert bench.main(["--only", stage, "--rows", "384", "--din", "256", "--batch", "20", "--steps", "6",
+                       "--warmup", "3"]) == 0
+    line = json.loads(capsys.readouterr().out)
+    assert line["stage"] == stage and line["ms"] > 0 and line["GB_per_s"] > 0
