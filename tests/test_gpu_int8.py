@@ -75,7 +75,7 @@ def test_encoders(d, kind):
         assert scale[-1].item() == 0 and not q[-1].any()
 
 
-@pytest.mark.parametrize("rows", [1, 2, 7, 8, 9, 149, 3001])
+@pytest.mark.parametrize("rows", [1, 2, 7, 8, 9, 149, 296, 297, 3001])
 @pytest.mark.parametrize("d", [64, 1024, 2048])
 def test_encoder_row_counts(rows, d):
     x = values(rows, d, "bf16", rows)
@@ -290,6 +290,66 @@ def test_gemm_is_the_same_every_time_and_reads_only_its_rows(ntok):
     for _ in range(3):
         y = qamw.qamw_int8_gemm(big_x[:ntok], xs[:ntok], big_w[:d_out], ws[:d_out])
         assert torch.equal(y, want)
+
+
+def test_offsets_past_32_bits():
+    """Inputs and outputs of more than 2^31 elements: the rows at the far end are those of a call
+    on them alone."""
+    d, rows = 32768, 70000
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty((rows, d), dtype=torch.bfloat16, device=DEV)
+    tail = slice(rows - 300, rows)
+    x.zero_()
+    x[tail] = torch.randn((300, d), generator=g, device=DEV).to(torch.bfloat16)
+    q, scale = qamw.qamw_int8_encode_tokens(x)
+    q_tail, scale_tail = qamw.qamw_int8_encode_tokens(x[tail].clone())
+    assert torch.equal(q[tail], q_tail) and torch.equal(scale[tail], scale_tail)
+    assert not q[:300].any() and not scale[:300].any()
+    h, qn, sn = qamw.qamw_rmsnorm_int8(x, torch.ones(d, dtype=torch.bfloat16, device=DEV), residual=x)
+    hn, qt, st = qamw.qamw_rmsnorm_int8(x[tail].clone(), torch.ones(d, dtype=torch.bfloat16, device=DEV),
+                                        residual=x[tail].clone())
+    assert torch.equal(h[tail], hn) and torch.equal(qn[tail], qt) and torch.equal(sn[tail], st)
+    del x, h, qn
+    # as weights (more than 2^31 bytes), for a token and for many
+    for ntok in (1, 3, 40, 300):
+        xq, xs = ints(ntok, d, ntok), scales(ntok, 1)
+        y = qamw.qamw_int8_gemm(xq, xs, q, scale, dtype=torch.float32)
+        assert torch.equal(y[:, tail], qamw.qamw_int8_gemm(xq, xs, q_tail, scale_tail, dtype=torch.float32))
+        assert not y[:, :1000].any()
+    del q, y
+    # outputs of more than 2^31 elements
+    for kind in (torch.bfloat16, torch.float32):
+        xq, xs, wq, ws = ints(65536, 64, 1), scales(65536, 2), ints(33000, 64, 3), scales(33000, 4)
+        y = qamw.qamw_int8_gemm(xq, xs, wq, ws, dtype=kind)
+        assert torch.equal(y[65000:], qamw.qamw_int8_gemm(xq[65000:], xs[65000:], wq, ws, dtype=kind))
+        assert torch.equal(y[:300], qamw.qamw_int8_gemm(xq[:300], xs[:300], wq, ws, dtype=kind))
+        del y
+
+
+def test_products_on_several_streams_at_once():
+    """CTAs, pairs and clusters that own tensor memory, and the codec's prefill product, all in
+    flight together."""
+    from tests.test_gpu_parity import codebook, gpu_encode, weights
+    cb = codebook(7)
+    Wt, _ = weights(512, 1024, 3, "bf16")
+    m, _ = gpu_encode(Wt, 1024, 64, 7, cb, None, 0.0, seed=1)
+    X = values(128, 1024, "bf16", 2)
+    calls = [lambda: qamw.qamw_decode_gemm(m, X)]
+    for ntok, d_out, d_in in ((300, 4096, 11008), (16, 4096, 11008), (1000, 4096, 1024), (1, 4096, 4096),
+                              (64, 11008, 4096)):
+        xq, xs, wq, ws = ints(ntok, d_in, 1), scales(ntok, 2), ints(d_out, d_in, 3), scales(d_out, 4)
+        calls.append(lambda a=(xq, xs, wq, ws): qamw.qamw_int8_gemm(*a))
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(12):
+        for s, c, o in zip(streams, calls, got):
+            with torch.cuda.stream(s):
+                o.append(c())
+    torch.cuda.synchronize()
+    for w, o in zip(want, got):
+        assert all(torch.equal(w, y) for y in o)
 
 
 def test_empty_calls():
