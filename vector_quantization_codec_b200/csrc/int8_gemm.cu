@@ -729,8 +729,8 @@ cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
                              int32_t* d_status, cudaStream_t stream) {
   // A few tokens: dot products straight from the weights' rows.  Measured against
-  // the tensor cores, us: 1 token 4096 -> 4096 4.7 (7.7), 4096 -> 32001 20.9 (23.1);
-  // 2 tokens 5.3 (7.8), 22.3 (23.3); 4 tokens 512 -> 1000 2.7 (3.3), 4096 -> 4096
+  // the tensor cores, us: 1 token 4096 -> 4096 3.8 (7.7), 4096 -> 32001 18.8 (23.1);
+  // 2 tokens 4.7 (7.8), 20.7 (23.3), 5120 -> 13824 15.2 (14.3); 4 tokens 512 -> 1000 2.7 (3.3), 4096 -> 4096
   // 8.1 (7.8), 4096 -> 32001 25.2 (23.3); rows of 64 bytes leave lanes idle: 1 token
   // 64 -> 50000 15.2 (4.9).
   if (d_in >= 256 && (ntok <= 2 || (ntok <= 4 && (int64_t)d_out * d_in <= 8 << 20)))
