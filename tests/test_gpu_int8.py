@@ -501,6 +501,39 @@ def test_captured_graphs_and_streams():
         assert torch.equal(g, g2) and torch.equal(u, u2)
 
 
+def test_inputs_freed_while_another_stream_still_reads_them():
+    """Inputs dropped right after a call on a busy stream: their memory must not be handed to the
+    next tensor of the current stream before the call has read it."""
+    ntok, d, out = 64, 4096, 512
+    wq, ws = ints(out, d, 1), scales(out, 2)
+    x0 = values(ntok, d, "bf16", 3)
+    q0, s0 = qamw.qamw_int8_encode_tokens(x0)
+    y0 = qamw.qamw_int8_gemm(q0, s0, wq, ws)
+    h0, n0, t0 = qamw.qamw_rmsnorm_int8(x0, torch.ones(d, dtype=torch.bfloat16, device=DEV), residual=x0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for kind in ("tokens", "norm", "gemm"):
+        a, b = (q0.clone(), s0.clone()) if kind == "gemm" else (x0.clone(), x0.clone())
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        if kind == "tokens":
+            got, want = qamw.qamw_int8_encode_tokens(a, stream=side), (q0, s0)
+        elif kind == "norm":
+            gain = torch.ones(d, dtype=torch.bfloat16, device=DEV)
+            side.wait_stream(torch.cuda.current_stream())
+            got, want = qamw.qamw_rmsnorm_int8(a, gain, residual=b, stream=side), (h0, n0, t0)
+            del gain
+        else:
+            got, want = (qamw.qamw_int8_gemm(a, b, wq, ws, stream=side.cuda_stream),), (y0,)
+        del a, b
+        junk = [torch.full((ntok, d), 1, dtype=t, device=DEV) for t in (torch.bfloat16, torch.int8) * 3]
+        junk += [torch.full((n,), 7.0, device=DEV) for n in (ntok, d, d // 2)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+        del junk
+
+
 def test_new_inputs_in_a_captured_graph():
     """A replay reads what its inputs hold then: other tokens, other weights."""
     xq, xs, wq, ws = ints(3, 512, 1), scales(3, 1), ints(200, 512, 2), scales(200, 2)

@@ -493,8 +493,10 @@ def qamw_decode_gemv_noalloc(m: EncodedMatrix, x: torch.Tensor, y: torch.Tensor,
 
 # ------------------------------------------------------- 8-bit integers (W8A8)
 # These wrappers check their tensors (type, shape, contiguity, one device), run
-# on the tensors' own device whichever is current, and allocate what they return
-# on the stream they launch on.
+# on the tensors' own device whichever is current, allocate what they return on
+# the stream they launch on, and with a stream of the caller's tell the allocator
+# that the tensors are used there.  (Ordering that stream behind whatever wrote
+# the inputs is the caller's.)
 
 _DTYPE_CODE = {torch.float32: QAMW_DTYPE_F32, torch.bfloat16: QAMW_DTYPE_BF16}
 
@@ -542,6 +544,16 @@ def _enter(index: int, stream):
     return ctx
 
 
+def _used_on(index: int, stream, *tensors) -> None:
+    """Tells the allocator that a call on `stream` (None: the current one, whose tensors these are
+    taken to be) reads or writes the tensors: their memory is not handed out again before."""
+    if stream is not None:
+        current = torch.cuda.current_stream(index)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(current)
+
+
 def _status_ptr(status: torch.Tensor | None, index: int):
     return None if status is None else _dense("status", status, torch.int32, status.shape, index)
 
@@ -573,6 +585,7 @@ def _int8_encode(fn, what: str, x, chan_scale, q, scale, status, stream):
     try:
         q, scale, qp, scp = _new_codes(x, q, scale)
         rc = fn(x.data_ptr(), code, rows, d, sp, qp, scp, _status_ptr(status, dev), _raw_stream(dev))
+        _used_on(dev, stream, x, chan_scale, q, scale, status)
     finally:
         if ctx is not None:
             ctx.close()
@@ -622,6 +635,7 @@ def qamw_rmsnorm_int8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-5,
         q, tok_scale, qp, sp = _new_codes(x, q, tok_scale)
         rc = _lib.qamw_rmsnorm_int8(x.data_ptr(), rp, code, gp, eps, rows, d, cp, hp, qp, sp,
                                     _status_ptr(status, dev), _raw_stream(dev))
+        _used_on(dev, stream, x, gain, residual, chan_scale, sum_out, q, tok_scale, status)
     finally:
         if ctx is not None:
             ctx.close()
@@ -657,6 +671,7 @@ def qamw_int8_gemm(xq: torch.Tensor, tok_scale: torch.Tensor, wq: torch.Tensor,
             yp = _dense("y", y, dtype, (ntok, d_out), dev)
         rc = _lib.qamw_int8_gemm(xp, sp, ntok, wp, rp, d_out, d_in, yp, code,
                                  _status_ptr(status, dev), _raw_stream(dev))
+        _used_on(dev, stream, xq, tok_scale, wq, row_scale, y, status)
     finally:
         if ctx is not None:
             ctx.close()
