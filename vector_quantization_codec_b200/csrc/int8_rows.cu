@@ -135,6 +135,17 @@ __device__ __forceinline__ void factors(const Int8RowsArgs& a, int vec, float2 (
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// The gain and the channel scales of eight columns on their way into L2.
+template <typename T, bool NORM>
+__device__ __forceinline__ void prefetch_factors(const Int8RowsArgs& a, int vec) {
+  if constexpr (NORM) prefetch_l2(static_cast<const char*>(a.gain) + (size_t)vec * 8 * sizeof(T));
+  if (a.s != nullptr) prefetch_l2(a.s + 8 * vec);
+}
+
 // max(|a|, |b|, |c|), NaN if one of them is: one instruction for two elements.
 __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   float d;
@@ -405,6 +416,22 @@ __global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
     fence_mbar_init();
   }
   __syncthreads();
+  // While the kernel ahead finishes, this CTA's first rows and its factors on their
+  // way into L2, whatever they hold by then; what counts is read after the wait.
+  // (8192 x 5120 bf16 with residual, back to back: 48.1 us without, 46.3 with.)
+  if (warp == nwarps) {
+    for (int j = lane; j < stages; j += 32) {
+      const int64_t row = blockIdx.x + (int64_t)j * gridDim.x;
+      if (row < a.rows) {
+        bulk_prefetch_l2(static_cast<const unsigned char*>(a.x) + row * row_bytes, row_bytes);
+        if constexpr (RES)
+          bulk_prefetch_l2(static_cast<const unsigned char*>(a.res) + row * row_bytes, row_bytes);
+      }
+    }
+  } else {
+    for (int v = t; v < nvec; v += n) prefetch_factors<T, NORM>(a, v);
+  }
+  __syncwarp();
   pdl_wait();
   pdl_trigger();
   int flags = 0, parity = 0, s = 0;
