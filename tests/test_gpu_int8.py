@@ -552,6 +552,51 @@ def test_new_inputs_in_a_captured_graph():
         assert torch.equal(y, check_gemm(xq, xs, wq, ws, torch.float32))
 
 
+@pytest.mark.parametrize("ntok", [1, 2, 4, 16, 40, 300])
+@pytest.mark.parametrize("d,out", [(256, 64), (2048, 1024), (4096, 4096)])
+def test_buffers_rewritten_back_to_back(d, out, ntok):
+    """Weights and tokens encoded into the same buffers again and again, each time followed at once
+    by the product that reads them (every kernel launched before the one ahead ends): each product
+    is that of its own step's values, neither older nor newer ones."""
+    steps = 6
+    W = [values(out, d, "bf16", 10 + i, 0.02) for i in range(steps)]
+    X = [values(ntok, d, "bf16", 50 + i) for i in range(steps)]
+    gain = torch.ones(d, dtype=torch.bfloat16, device=DEV)
+    want = []
+    for w, x in zip(W, X):
+        a, b = qamw.qamw_int8_encode_weights(w), qamw.qamw_rmsnorm_int8(x, gain)
+        torch.cuda.synchronize()
+        want.append(qamw.qamw_int8_gemm(*b, *a))
+        torch.cuda.synchronize()
+    wq, ws = torch.zeros((out, d), dtype=torch.int8, device=DEV), torch.zeros(out, device=DEV)
+    xq, xs = torch.zeros((ntok, d), dtype=torch.int8, device=DEV), torch.zeros(ntok, device=DEV)
+    y = [torch.zeros_like(want[0]) for _ in range(4 * steps)]
+    torch.cuda.synchronize()
+    for k, o in enumerate(y):
+        qamw.qamw_rmsnorm_int8(X[k % steps], gain, q=xq, tok_scale=xs)
+        qamw.qamw_int8_encode_weights(W[k % steps], q=wq, row_scale=ws)
+        qamw.qamw_int8_gemm(xq, xs, wq, ws, y=o)
+    torch.cuda.synchronize()
+    for k, o in enumerate(y):
+        assert torch.equal(o, want[k % steps]), k
+    # captured: launches closer together still, tokens last
+    def step(k):
+        qamw.qamw_int8_encode_weights(W[k], q=wq, row_scale=ws)
+        qamw.qamw_rmsnorm_int8(X[k], gain, q=xq, tok_scale=xs)
+        qamw.qamw_int8_gemm(xq, xs, wq, ws, y=y[k])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for k in range(steps):
+            step(k)
+    for _ in range(3):
+        for o in y:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for k in range(steps):
+            assert torch.equal(y[k], want[k]), k
+
+
 def test_product_feeds_the_decode_products():
     """In one stream with the codec's own kernels, each launched before the one ahead ends: the
     8-bit product's output as the input of a decode-GEMV and of the prefill product."""
