@@ -728,12 +728,15 @@ cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap
 cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
                              int32_t* d_status, cudaStream_t stream) {
-  // A few tokens: dot products straight from the weights' rows.  Measured against
-  // the tensor cores, us: 1 token 4096 -> 4096 3.8 (7.7), 4096 -> 32001 18.8 (23.1);
-  // 2 tokens 4.7 (7.8), 20.7 (23.3), 5120 -> 13824 15.2 (14.3); 4 tokens 512 -> 1000 2.7 (3.3), 4096 -> 4096
-  // 8.1 (7.8), 4096 -> 32001 25.2 (23.3); rows of 64 bytes leave lanes idle: 1 token
-  // 64 -> 50000 15.2 (4.9).
-  if (d_in >= 256 && (ntok <= 2 || (ntok <= 4 && (int64_t)d_out * d_in <= 8 << 20)))
+  // A few tokens: the weights' rows straight from global memory.  Measured against
+  // the kernel below, us: 1 token 4096 -> 4096 3.8 (7.7), 4096 -> 32001 18.8 (23.1);
+  // 2 tokens 4.7 (7.8), 20.7 (23.3), 5120 -> 13824 15.2 (14.3); 5 tokens 4096 -> 4096
+  // 6.3 (7.3), 4096 -> 11008 10.4 (11.5), 4096 -> 32001 22.0 (23.2), 2048 -> 64 2.3
+  // (4.2).  Short rows leave lanes idle (1 token 64 -> 50000 15.2 against 4.9; 8
+  // tokens 256 -> 5632 3.4 against 3.0); with three tokens and more long ones take too
+  // many steps, and too much shared memory, per 16 rows (5 tokens 8192 -> 1024 6.5
+  // against 5.7, 11008 -> 4096 12.5 against 11.8).
+  if ((ntok <= 2 && d_in >= 256) || (ntok <= 8 && d_in >= 512 && d_in <= 6144))
     return launch_int8_gemv(d_x, d_x_scale, ntok, d_w, d_w_scale, d_out, d_in, d_y, dtype, stream);
   const Int8Plan p = plan_int8(ntok, d_out, d_in,
                                dtype == QAMW_DTYPE_BF16 && d_out % 8 == 0 &&

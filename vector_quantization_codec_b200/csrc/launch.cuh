@@ -122,7 +122,7 @@ cudaError_t launch_rmsnorm_int8(const void* d_x, const void* d_residual, int dty
                                 const void* d_gain, float eps, int64_t rows, int d,
                                 const uint16_t* d_chan_scale, void* d_sum, int8_t* d_q,
                                 float* d_scale, int32_t* d_status, cudaStream_t stream);
-// The product of up to four tokens (called by launch_int8_gemm).
+// The product of up to eight tokens (called by launch_int8_gemm; three and more: d_in from 512 to 6144).
 cudaError_t launch_int8_gemv(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
                              cudaStream_t stream);
