@@ -38,14 +38,22 @@ constexpr int kCopyWarp = 9;          // one thread issues the copies
 constexpr int kStoreWarp = 10;         // one thread issues the stores of staged outputs
 constexpr int kThreads = 11 * 32;
 
-// Shared memory of the stages, and of what follows them when outputs are staged:
-// three blocks of 32 tokens x 128 channels of bf16.
-constexpr uint32_t kSmem = 216u * 1024u;
 // Batches up to this size write their outputs directly: too few to fill a block.
 constexpr int kFewTokens = 16;
-constexpr int kBlockTok = 32;             // tokens per staged block of outputs
+constexpr int kBlockTok = 64;  // tokens per staged block of outputs (of 128 channels, bf16)
 constexpr uint32_t kBlock = kBlockTok * kRowsM * 2;
-constexpr int kBlocks = 3;
+constexpr int kBlocks = 2;
+// Shared memory, all of it dynamic so that its start is aligned for the swizzle:
+// stages and (at the end of the same room) the staged blocks; then barriers,
+// token scales and the tensor-memory address.
+constexpr uint32_t kSmem = 224u * 1024u;
+struct Int8Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages], accfull[2], accempty[2], fin;
+  float xs[2][2][128];  // [tile parity][half of the epilogue warps]
+  uint32_t tmem_slot;
+};
+constexpr size_t kSmemAll = kSmem + sizeof(Int8Shared);
+static_assert(kSmemAll <= 227 * 1024, "shared memory of an SM");
 constexpr int kMaxSplits = 8;             // CTAs of a cluster
 
 struct Int8GemmArgs {
@@ -310,10 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_int8_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_y, const Int8GemmArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], accfull[2], accempty[2], fin;
-  __shared__ __align__(16) float xs_tile[kEpiWarps][128];
-  __shared__ uint32_t tmem_slot;
+  unsigned char* smem = smem_raw;
+  Int8Shared& sh = *reinterpret_cast<Int8Shared*>(smem + kSmem);
+  uint64_t *full = sh.full, *empty = sh.empty, *accfull = sh.accfull, *accempty = sh.accempty;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t crank = CG == 2 || a.splits > 1 ? cluster_rank() : 0u;
   // place in the pair, split of the tile's chunks, the pair's leader and mask
@@ -337,17 +344,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&accfull[b], 1);
       mbar_init(&accempty[b], kEpiWarps * CG);
     }
-    mbar_init(&fin, 1);
+    mbar_init(&sh.fin, 1);
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) tmem_alloc<CG>(&tmem_slot, cols);
+  if (warp == kMmaWarp) tmem_alloc<CG>(&sh.tmem_slot, cols);
   tc_fence_before();
   if (CG == 2)
     cluster_sync();
   else
     __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = sh.tmem_slot;
   // every operand and scale may come from the kernel ahead (which is why the scales
   // are not read through the read-only path)
   pdl_wait();
@@ -439,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) flags |= QAMW_STATUS_TIMEOUT;
       // every MMA is done before the tensor memory and the stages are given up
-      commit<CG>(&fin, 1u << leader);
-      if (!mbar_wait_bounded(&fin, 0)) flags |= QAMW_STATUS_TIMEOUT;
+      commit<CG>(&sh.fin, 1u << leader);
+      if (!mbar_wait_bounded(&sh.fin, 0)) flags |= QAMW_STATUS_TIMEOUT;
     }
   } else if (warp == kStoreWarp) {
     if (a.staged) {
@@ -453,27 +460,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t0 = (int)(tile - m * a.tok_tiles) * a.nt;
         const int nt = min(a.nt, a.ntok - t0);
         for (int c = 0; c < nt; c += kBlockTok) {
-          // the block that comes next is free once its stores, the last but one, have
-          // read it: the epilogue warps write it behind this barrier
-          if (one) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          // the block that comes next is free once its stores have read it: the epilogue
+          // warps write it behind this barrier
+          if (one) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           __syncwarp();
           asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps + 32) : "memory");
           if (one) {
             const uint32_t buf = blocks + block * kBlock;
-            if (i0 < a.d_out) store_box(&map_y, i0, t0 + c, buf);
-            if (i0 + 64 < a.d_out) store_box(&map_y, i0 + 64, t0 + c, buf + kBlock / 2);
+            // 64 channels x 32 tokens a store: a tile may end in the middle of a block
+            for (int k = 0; k < 2; ++k)
+              for (int h = 0; h < 2; ++h)
+                if (i0 + 64 * k < a.d_out && c + 32 * h < nt)
+                  store_box(&map_y, i0 + 64 * k, t0 + c + 32 * h, buf + k * (kBlock / 2) + h * (kBlock / 4));
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
-          block = block == kBlocks - 1 ? 0 : block + 1;
+          block ^= 1;
         }
       }
       if (one) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   } else if (a.splits == 1) {
     T* y = reinterpret_cast<T*>(a.y);
-    // warp w: lanes (channels) 32 (w % 4) .. + 31, columns 16 (w / 4) + 32 k .. + 15
+    // warp w: lanes (channels) 32 (w % 4) .. + 31, columns 32 k + 16 (w / 4) .. + 15
     const int q4 = warp & 3, half = warp >> 2;
-    float* xs = xs_tile[warp];
     const uint32_t blocks = smem_u32(smem) + kSmem - kBlocks * kBlock;
     int n = 0, block = 0;
     bool alive = true;
@@ -492,17 +501,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t k = i0 + 32 * q4 + (lane >> 2) + 8 * g;
         wg[g] = a.staged && k < a.d_out ? a.ws[k] : 0.f;
       }
-      {  // the scales of the warp's tokens, all loads in flight together: entry k is
-         // token 32 (k / 16) + 16 half + k % 16 of the tile
-        float x4[4];
+      // the scales of the warp's tokens, all loads in flight together: entry k is token
+      // 32 (k / 16) + 16 half + k % 16 of the tile
+      float x4[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int c = 64 * k + 32 * (lane >> 4) + 16 * half + (lane & 15);
-          x4[k] = c < nt ? a.xs[t0 + c] : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) xs[lane + 32 * k] = x4[k];
-        __syncwarp();
+      for (int k = 0; k < 4; ++k) {
+        const int c = 64 * k + 32 * (lane >> 4) + 16 * half + (lane & 15);
+        x4[k] = c < nt ? a.xs[t0 + c] : 0.f;
       }
       // one lane polls: 32 pollers a warp would slow the other roles' waits.  A
       // wait that gives up is not repeated; the warps still meet at the barriers.
@@ -511,34 +516,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         flags |= QAMW_STATUS_TIMEOUT;
         alive = false;
       }
+      // (the four warps of a half write the same; a warp that gets here has seen the
+      // others done with the tile before the last, whose scales these replace)
+      float* xs = sh.xs[b][half];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) xs[lane + 32 * k] = x4[k];
+      __syncwarp();
       tc_fence_after();
       if (a.staged) {
-        // 32 tokens x 128 channels of all eight warps go through shared memory and
+        // 64 tokens x 128 channels of all eight warps go through shared memory and
         // leave by tensor stores.  (Direct 2-byte stores, or shuffles to wider ones,
         // kept the load-store unit busy for 4300 cycles a tile of 256 tokens.)
         for (int c = 0; c < nt; c += kBlockTok) {
           const uint32_t buf = blocks + block * kBlock;
-          block = block == kBlocks - 1 ? 0 : block + 1;
-          const int cw = c + 16 * half;
-          if (cw < nt) {
-            int v[2][8];
-            tmem_ld_frag(tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(b * a.nt + cw), v[0]);
-            tmem_ld_frag(tmem + ((uint32_t)(32 * q4 + 16) << 16) + (uint32_t)(b * a.nt + cw), v[1]);
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          block ^= 1;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float2 x2 = *reinterpret_cast<const float2*>(xs + c / 2 + 8 * j + 2 * (lane & 3));
-              uint32_t w[4];
+          for (int sb = 0; sb < 2; ++sb) {
+            const int cw = c + 32 * sb + 16 * half;
+            if (cw < nt) {
+              int v[2][8];
+              tmem_ld_frag(tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(b * a.nt + cw), v[0]);
+              tmem_ld_frag(tmem + ((uint32_t)(32 * q4 + 16) << 16) + (uint32_t)(b * a.nt + cw), v[1]);
+              asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const int lo = v[g >> 1][4 * j + 2 * (g & 1)], hi = v[g >> 1][4 * j + 2 * (g & 1) + 1];
-                const float2 f = mul2(make_float2((float)lo, (float)hi), mul2(x2, make_float2(wg[g], wg[g])));
-                w[g] = pack_bf16x2(f.x, f.y);
+              for (int j = 0; j < 2; ++j) {
+                const float2 x2 =
+                    *reinterpret_cast<const float2*>(xs + c / 2 + 16 * sb + 8 * j + 2 * (lane & 3));
+                uint32_t w[4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  const int lo = v[g >> 1][4 * j + 2 * (g & 1)], hi = v[g >> 1][4 * j + 2 * (g & 1) + 1];
+                  const float2 f = mul2(make_float2((float)lo, (float)hi), mul2(x2, make_float2(wg[g], wg[g])));
+                  w[g] = pack_bf16x2(f.x, f.y);
+                }
+                // block g of eight channels = 16-byte unit 4 (q4 % 2) + g of the 64
+                // channels q4 / 2; swizzled as the tensor store expects
+                const int tok = 32 * sb + 16 * half + 8 * j + (lane & 7), unit = 4 * (q4 & 1) + (lane >> 3);
+                stmatrix4_t(buf + (uint32_t)((q4 >> 1) * (kBlock / 2) + tok * 128 + ((unit ^ (tok & 7)) << 4)), w);
               }
-              // block g of eight channels = 16-byte unit 4 (q4 % 2) + g of the 64
-              // channels q4 / 2; swizzled as the tensor store expects
-              const int tok = 16 * half + 8 * j + (lane & 7), unit = 4 * (q4 & 1) + (lane >> 3);
-              stmatrix4_t(buf + (uint32_t)((q4 >> 1) * (kBlock / 2) + tok * 128 + ((unit ^ (tok & 7)) << 4)), w);
             }
           }
           fence_proxy_async_smem();
@@ -546,13 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const int64_t pitch = a.d_out;
-        T* out = y + (t0 + 16 * half) * pitch + i;
-        for (int c = 16 * half; c < nt; c += 32, out += 32 * pitch) {
+        for (int c = 16 * half; c < nt; c += 32) {
           int v[16];
           tmem_ld16(tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(b * a.nt + c), v);
+          T* out = y + (t0 + c) * pitch + i;
+          const float* xc = xs + c / 32 * 16;
           float f[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) f[e] = __fmul_rn((float)v[e], __fmul_rn(xs[c / 32 * 16 + e], wi));
+          for (int e = 0; e < 16; ++e) f[e] = __fmul_rn((float)v[e], __fmul_rn(xc[e], wi));
           if (mine) {
             if (c + 16 <= nt) {
 #pragma unroll
@@ -583,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = 0; e < 4; ++e) split_w[e] = split_i + e < a.d_out ? a.ws[split_i + e] : 0.f;
     {
       const int t = split_t0 + split + a.splits * (warp + kEpiWarps * lane);
-      xs_tile[warp][lane] = t < a.ntok ? a.xs[t] : 0.f;
+      (&sh.xs[0][0][0])[32 * warp + lane] = t < a.ntok ? a.xs[t] : 0.f;
     }
     // the CTA's partial sums into its own shared memory (the stages are free:
     // every MMA that reads them is done), [token][channel]
@@ -604,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     if (warp < kEpiWarps)
       add_partials<CG, T>(a, split_i, split_t0, split, rank, smem_u32(smem), warp, lane, split_w,
-                          xs_tile[warp]);
+                          &sh.xs[0][0][0] + 32 * warp);
   }
   __syncwarp();
   if (CG == 2 || a.splits > 1)
@@ -624,7 +640,7 @@ bool encode_out_map(CUtensorMap* map, void* p, int64_t rows, int d_out) {
   if (!enc) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)d_out, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)d_out * 2};
-  const cuuint32_t boxes[2] = {64, kBlockTok};
+  const cuuint32_t boxes[2] = {64, 32};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, boxes, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -693,7 +709,7 @@ Int8Plan plan_int8(int ntok, int d_out, int d_in, bool bf16_rows) {
   }
   // the wait for a stage and its commit cost the MMA thread about 240 cycles:
   // several chunks per stage, as long as three stages fit
-  p.staged = bf16_rows && p.splits == 1 && ntok > kFewTokens && (p.nt % kBlockTok == 0 || ntok <= p.nt);
+  p.staged = bf16_rows && p.splits == 1 && ntok > kFewTokens && (p.nt % 32 == 0 || ntok <= p.nt);
   const uint32_t ring = kSmem - (p.staged ? kBlocks * kBlock : 0);
   p.boxes = 4;
   while (p.boxes > 1 && ring / (box_bytes(p.cg, p.nt) * p.boxes) < 3) --p.boxes;
@@ -708,7 +724,7 @@ cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap
   // all of the ring, whatever the stages need of it: one CTA that owns tensor
   // memory per SM, so that an allocation never waits for a CTA that could be
   // waiting for it
-  constexpr size_t smem = kSmem + 1024;
+  constexpr size_t smem = kSmemAll;
   cudaError_t err = allow_smem(reinterpret_cast<const void*>(fn), smem);
   if (err != cudaSuccess) return err;
   const int per = CG * p.splits;
