@@ -520,7 +520,9 @@ def _rows_of(name: str, x: torch.Tensor) -> int:
     return code
 
 
-# The current stream's handle without building a Stream object (a few microseconds a call).
+# The current stream's handle without building a Stream object (a few microseconds a call), and
+# the current device without the check that CUDA is up, which a tensor on a GPU answers.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -529,7 +531,7 @@ def _enter(index: int, stream):
     """Makes GPU `index` current and `stream` (when given) its current stream, so that what is
     allocated next belongs to the stream it is used on; None when that is so already, else the
     context to close."""
-    if stream is None and torch.cuda.current_device() == index:
+    if stream is None and _current_device() == index:
         return None
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(index))
@@ -544,18 +546,17 @@ def _enter(index: int, stream):
     return ctx
 
 
-def _used_on(index: int, stream, *tensors) -> None:
-    """Tells the allocator that a call on `stream` (None: the current one, whose tensors these are
-    taken to be) reads or writes the tensors: their memory is not handed out again before."""
-    if stream is not None:
-        current = torch.cuda.current_stream(index)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(current)
+def _used_on(index: int, *tensors) -> None:
+    """Tells the allocator that a call on the stream that the caller gave, current here, reads or
+    writes the tensors: their memory is not handed out again before."""
+    current = torch.cuda.current_stream(index)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(current)
 
 
-def _status_ptr(status: torch.Tensor | None, index: int):
-    return None if status is None else _dense("status", status, torch.int32, status.shape, index)
+def _status_ptr(status: torch.Tensor, index: int) -> int:
+    return _dense("status", status, torch.int32, status.shape, index)
 
 
 def _new_codes(x, q, scale):
@@ -584,8 +585,10 @@ def _int8_encode(fn, what: str, x, chan_scale, q, scale, status, stream):
     ctx = _enter(dev, stream)
     try:
         q, scale, qp, scp = _new_codes(x, q, scale)
-        rc = fn(x.data_ptr(), code, rows, d, sp, qp, scp, _status_ptr(status, dev), _raw_stream(dev))
-        _used_on(dev, stream, x, chan_scale, q, scale, status)
+        stp = None if status is None else _status_ptr(status, dev)
+        rc = fn(x.data_ptr(), code, rows, d, sp, qp, scp, stp, _raw_stream(dev))
+        if stream is not None:
+            _used_on(dev, x, chan_scale, q, scale, status)
     finally:
         if ctx is not None:
             ctx.close()
@@ -633,9 +636,11 @@ def qamw_rmsnorm_int8(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-5,
             sum_out = torch.empty_like(x)
             hp = sum_out.data_ptr()
         q, tok_scale, qp, sp = _new_codes(x, q, tok_scale)
-        rc = _lib.qamw_rmsnorm_int8(x.data_ptr(), rp, code, gp, eps, rows, d, cp, hp, qp, sp,
-                                    _status_ptr(status, dev), _raw_stream(dev))
-        _used_on(dev, stream, x, gain, residual, chan_scale, sum_out, q, tok_scale, status)
+        stp = None if status is None else _status_ptr(status, dev)
+        rc = _lib.qamw_rmsnorm_int8(x.data_ptr(), rp, code, gp, eps, rows, d, cp, hp, qp, sp, stp,
+                                    _raw_stream(dev))
+        if stream is not None:
+            _used_on(dev, x, gain, residual, chan_scale, sum_out, q, tok_scale, status)
     finally:
         if ctx is not None:
             ctx.close()
@@ -665,13 +670,14 @@ def qamw_int8_gemm(xq: torch.Tensor, tok_scale: torch.Tensor, wq: torch.Tensor,
     ctx = _enter(dev, stream)
     try:
         if y is None:
-            y = xq.new_empty((ntok, d_out), dtype=dtype)
+            y = xq.new_empty(ntok, d_out, dtype=dtype)
             yp = y.data_ptr()
         else:
             yp = _dense("y", y, dtype, (ntok, d_out), dev)
-        rc = _lib.qamw_int8_gemm(xp, sp, ntok, wp, rp, d_out, d_in, yp, code,
-                                 _status_ptr(status, dev), _raw_stream(dev))
-        _used_on(dev, stream, xq, tok_scale, wq, row_scale, y, status)
+        stp = None if status is None else _status_ptr(status, dev)
+        rc = _lib.qamw_int8_gemm(xp, sp, ntok, wp, rp, d_out, d_in, yp, code, stp, _raw_stream(dev))
+        if stream is not None:
+            _used_on(dev, xq, tok_scale, wq, row_scale, y, status)
     finally:
         if ctx is not None:
             ctx.close()
