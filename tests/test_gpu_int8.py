@@ -256,6 +256,12 @@ def test_gemm_layer_shapes(shape, kind):
     check_gemm(ints(ntok, d_in, 1), scales(ntok, 2), ints(d_out, d_in, 3), scales(d_out, 4), T[kind])
 
 
+@pytest.mark.parametrize("ntok", [290, 515, 777, 900, 1100, 2499])
+def test_gemm_several_rounds_of_tiles(ntok):
+    for d_out, d_in, kind in ((19000, 1024, "bf16"), (13824, 192, "bf16"), (19001, 320, "f32"), (5001, 2048, "bf16")):
+        check_gemm(ints(ntok, d_in, ntok), scales(ntok, 1), ints(d_out, d_in, 5), scales(d_out, 2), T[kind])
+
+
 @pytest.mark.parametrize("ntok", [1, 12, 100, 300])
 def test_gemm_extreme_sums(ntok):
     """Sums of +-2^29 (all 256 values of int8 are allowed) and exact zeros."""
