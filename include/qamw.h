@@ -149,6 +149,17 @@ QAMW_API const char *qamw_status_string(int code);
 QAMW_API int qamw_selftest_wait_timeout(unsigned tries, int32_t *d_status, long long *d_cycles,
                                         void *stream);
 
+/* qamw_selftest_rmsnorm_int8: qamw_rmsnorm_int8 whose waits for rows on their
+ *   way into shared memory (large batches of d above 512) give up after `tries`
+ *   polls (0 .. 2^18).  A CTA that gives up writes no code and no scale of the
+ *   row it waited for and of its rows after that; of the first of them, h may
+ *   be written in part.  Errors: those of qamw_rmsnorm_int8, QAMW_ERR_INVALID
+ *   for tries out of range or a null status. */
+QAMW_API int qamw_selftest_rmsnorm_int8(unsigned tries, const void *d_x, const void *d_residual,
+                                        int dtype, const void *d_gain, float eps, int ntok, int d,
+                                        const uint16_t *d_chan_scale, void *d_sum, int8_t *d_q,
+                                        float *d_tok_scale, int32_t *d_status, void *stream);
+
 /* ------------------------------------------------------------------ calls */
 
 /* Section 3.6 eq. (2): Lloyd iterations for the joint 2D codebook.
@@ -413,8 +424,9 @@ QAMW_API int qamw_decode_gemv_noalloc(const qamw_matrix *m, const uint16_t *d_x,
  * every operation rounded once to fp32; a row with a < 2^-100 (a row of zeros)
  * gives q = 0, scale = 0, and a row with a NaN or Inf among its values gives
  * q = 0, scale = NaN (flagged NONFINITE), which the product carries to that
- * row's outputs alone.  d and d_in are multiples of 64 up to 32768; a count of
- * 0 rows is a no-op.  Inputs and outputs may not overlap, except where stated.
+ * row's outputs alone.  A large batch may also be flagged TIMEOUT: a row's copy
+ * did not arrive (qamw_selftest_rmsnorm_int8 says what is written then).  d and
+ * d_in are multiples of 64 up to 32768; a count of 0 rows is a no-op.  Inputs and outputs may not overlap, except where stated.
  * None of these calls needs a workspace.  d_chan_scale: binary16 [d],
  * 16B-aligned, non-zero; NULL stands for s = 1.
  *

@@ -107,3 +107,10 @@ def test_stated_fp32_steps_follow_the_mathematics(kind):
 def test_gemm_c_types_take_null():
     assert L.qamw_int8_gemm(None, None, 0, None, None, 0, 64, None, F32, None, None) == OK
     assert isinstance(L, C.CDLL)
+
+
+@pytest.mark.parametrize("tries,st,eps,rc", [(0, None, 1e-5, INVALID), ((1 << 18) + 1, FAKE, 1e-5, INVALID),
+                                             (0, FAKE, 0.0, INVALID)])
+def test_giving_up_check_argument_errors(tries, st, eps, rc):
+    assert L.qamw_selftest_rmsnorm_int8(tries, FAKE, FAKE, BF16, FAKE, eps, 4, 128, None, FAKE, FAKE, FAKE,
+                                        st, None) == rc

@@ -163,6 +163,21 @@ int check_int8_rows(const void* d_x, int dtype, int64_t rows, int d, const uint1
 
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? QAMW_OK : QAMW_ERR_CUDA; }
 
+int rmsnorm_int8(unsigned tries, const void* d_x, const void* d_residual, int dtype,
+                 const void* d_gain, float eps, int ntok, int d, const uint16_t* d_chan_scale,
+                 void* d_sum, int8_t* d_q, float* d_tok_scale, int32_t* d_status, void* stream) {
+  const int rc = check_int8_rows(d_x, dtype, ntok, d, d_chan_scale, d_q, d_tok_scale);
+  if (rc != QAMW_OK) return rc;
+  // not eps >= FLT_MIN also refuses NaN
+  if (!(eps >= FLT_MIN) || !std::isfinite(eps)) return QAMW_ERR_INVALID;
+  if (ntok == 0) return QAMW_OK;
+  if (!d_gain || (d_residual == nullptr) != (d_sum == nullptr)) return QAMW_ERR_INVALID;
+  if (!aligned16(d_gain) || !aligned16(d_residual) || !aligned16(d_sum)) return QAMW_ERR_ALIGN;
+  return cuda_rc(launch_rmsnorm_int8(d_x, d_residual, dtype, d_gain, eps, ntok, d, d_chan_scale,
+                                     d_sum, d_q, d_tok_scale, d_status,
+                                     static_cast<cudaStream_t>(stream), tries));
+}
+
 }  // namespace
 
 extern "C" {
@@ -488,16 +503,17 @@ int qamw_int8_encode_tokens(const void* d_x, int dtype, int ntok, int d,
 int qamw_rmsnorm_int8(const void* d_x, const void* d_residual, int dtype, const void* d_gain,
                       float eps, int ntok, int d, const uint16_t* d_chan_scale, void* d_sum,
                       int8_t* d_q, float* d_tok_scale, int32_t* d_status, void* stream) {
-  const int rc = check_int8_rows(d_x, dtype, ntok, d, d_chan_scale, d_q, d_tok_scale);
-  if (rc != QAMW_OK) return rc;
-  // not eps >= FLT_MIN also refuses NaN
-  if (!(eps >= FLT_MIN) || !std::isfinite(eps)) return QAMW_ERR_INVALID;
-  if (ntok == 0) return QAMW_OK;
-  if (!d_gain || (d_residual == nullptr) != (d_sum == nullptr)) return QAMW_ERR_INVALID;
-  if (!aligned16(d_gain) || !aligned16(d_residual) || !aligned16(d_sum)) return QAMW_ERR_ALIGN;
-  return cuda_rc(launch_rmsnorm_int8(d_x, d_residual, dtype, d_gain, eps, ntok, d, d_chan_scale,
-                                     d_sum, d_q, d_tok_scale, d_status,
-                                     static_cast<cudaStream_t>(stream)));
+  return rmsnorm_int8(kSpinLimit, d_x, d_residual, dtype, d_gain, eps, ntok, d, d_chan_scale, d_sum,
+                      d_q, d_tok_scale, d_status, stream);
+}
+
+int qamw_selftest_rmsnorm_int8(unsigned tries, const void* d_x, const void* d_residual, int dtype,
+                               const void* d_gain, float eps, int ntok, int d,
+                               const uint16_t* d_chan_scale, void* d_sum, int8_t* d_q,
+                               float* d_tok_scale, int32_t* d_status, void* stream) {
+  if (tries > kSpinLimit || !d_status) return QAMW_ERR_INVALID;
+  return rmsnorm_int8(tries, d_x, d_residual, dtype, d_gain, eps, ntok, d, d_chan_scale, d_sum, d_q,
+                      d_tok_scale, d_status, stream);
 }
 
 int qamw_int8_gemm(const int8_t* d_x, const float* d_tok_scale, int ntok, const int8_t* d_w,

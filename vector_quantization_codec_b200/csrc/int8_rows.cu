@@ -46,6 +46,7 @@ struct Int8RowsArgs {
   int32_t* status;
   int64_t rows;
   int d;
+  unsigned tries;  // polls of a worker's wait for a row (k_int8_ring)
   float eps;
   float one;   // 1 (see pack_rounded)
   int divide;  // tokens and norm: c = (g or 1) / s, weights: c = s
@@ -396,8 +397,15 @@ cudaError_t run_rows(const Int8RowsArgs& a, int threads, cudaStream_t stream) {
 // right behind it.  The last warp has no vectors: it issues the copies and forms
 // the scales (a chain of divisions and a root, some 300 cycles) while the others
 // go on to the next row.
+//
+// A worker whose wait for a row gives up reads nothing of it, sets the row's flag and
+// puts kGaveUp, above every value's bits, in the place of its largest |v|.  Behind the
+// row's barrier the helper sees the flag before it refills a stage, and the reduction
+// tells the workers: all leave the loop together, before a code or scale of the row is
+// written, and the helper lets its copies in flight land.
 constexpr int kRingVec = 2;
 constexpr int kRingMax = 8;
+constexpr uint32_t kGaveUp = 0xffffffffu;
 // Threads of a CTA at most; fewer with fp32 and a residual (d <= 13312 then),
 // which needs more than 64 registers.
 template <typename T, bool RES>
@@ -410,15 +418,15 @@ __global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
     k_int8_ring(const Int8RowsArgs a, int stages) {
   __shared__ RowSlots slots[2];
   __shared__ uint64_t full[kRingMax];
-  __shared__ int gave_up;
+  __shared__ volatile int gave_up[2];  // by row parity, as the slots
   extern __shared__ __align__(128) unsigned char ring[];
   const int n = blockDim.x - 32, t = threadIdx.x, nvec = a.d / 8;
   const int lane = t & 31, warp = t >> 5, nwarps = n >> 5;
   const uint32_t row_bytes = (uint32_t)a.d * sizeof(T), stage = row_bytes * (RES ? 2 : 1);
   if (t == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
-    gave_up = 0;
     fence_mbar_init();
+    gave_up[0] = gave_up[1] = 0;
   }
   __syncthreads();
   // While the kernel ahead finishes, this CTA's first rows and its factors on their
@@ -452,8 +460,14 @@ __global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
     };
     if (lane == 0)
       for (int j = 0; j < stages; ++j) fetch(blockIdx.x + (int64_t)j * gridDim.x, j);
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    for (int64_t row = blockIdx.x, j = 0; row < a.rows; row += gridDim.x, ++j) {
       __syncthreads();
+      if (gave_up[parity]) {  // this CTA's rows j .. j + stages - 1 are in flight
+        const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
+        for (int64_t i = j; i < min(mine, j + stages); ++i)
+          mbar_wait_bounded(&full[i % stages], (uint32_t)(i / stages) & 1u);
+        break;
+      }
       if (lane == 0) fetch(row + (int64_t)stages * gridDim.x, s);
       const RowSlots& r = slots[parity];
       const uint32_t top = __reduce_max_sync(0xffffffffu, lane < nwarps ? r.top[lane] : 0u);
@@ -462,45 +476,38 @@ __global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
       parity ^= 1;
       if (++s == stages) s = 0;
     }
-    if (gave_up) {  // no copy in flight at exit, here too
-      const int64_t mine = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x;
-      for (int64_t j = mine > stages ? mine - stages : 0; j < mine; ++j)
-        if (!mbar_wait_bounded(&full[j % stages], (uint32_t)(j / stages) & 1u)) break;
-    }
   } else {
     float2 c[kRingVec][4];
 #pragma unroll
     for (int i = 0; i < kRingVec; ++i)
       if (t + i * n < nvec) factors<T, NORM>(a, t + i * n, c[i]);
     uint32_t u = 0;
-    bool alive = true;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
       const int64_t base = row * nvec;
-      // a wait that gives up is not repeated; the row's barriers are still met
-      if (alive && !mbar_wait_bounded(&full[s], u & 1u)) {
-        alive = false;
-        gave_up = 1;
-        flags |= QAMW_STATUS_TIMEOUT;
-      }
       const unsigned char* src = ring + (size_t)s * stage;
       float2 v[kRingVec][4];
       RowStat r;
       r.sum = make_float2(0.f, 0.f);
-      r.top = 0.f;
+      r.top = __uint_as_float(kGaveUp);
+      if (mbar_wait_bounded(&full[s], u & 1u, a.tries)) {
+        r.top = 0.f;
 #pragma unroll
-      for (int i = 0; i < kRingVec; ++i) {
-        const int at = t + i * n;
-        if (at < nvec) {
-          Raw8<T> h;
-          h.load(src, at);
-          if constexpr (RES) {
-            Raw8<T> o;
-            o.load(src + row_bytes, at);
-            h.add(o);
-            h.store(a.sum, base + at);
+        for (int i = 0; i < kRingVec; ++i) {
+          const int at = t + i * n;
+          if (at < nvec) {
+            Raw8<T> h;
+            h.load(src, at);
+            if constexpr (RES) {
+              Raw8<T> o;
+              o.load(src + row_bytes, at);
+              h.add(o);
+              h.store(a.sum, base + at);
+            }
+            take<NORM>(r, h, c[i], v[i]);
           }
-          take<NORM>(r, h, c[i], v[i]);
         }
+      } else {
+        gave_up[parity] = 1;
       }
       RowSlots& slot = slots[parity];
       uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(r.top));
@@ -518,6 +525,9 @@ __global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
 #pragma unroll
         for (int i = 0; i < kRingVec; ++i)
           if (t + i * n < nvec) put_q(a, base + t + i * n, v[i], o);
+      } else if (top == kGaveUp) {
+        flags |= QAMW_STATUS_TIMEOUT;
+        break;
       } else {
 #pragma unroll
         for (int i = 0; i < kRingVec; ++i)
@@ -574,6 +584,7 @@ cudaError_t launch_int8_encode(const void* d_x, int dtype, int64_t rows, int d,
                                const uint16_t* d_chan_scale, bool divide, int8_t* d_q,
                                float* d_scale, int32_t* d_status, cudaStream_t stream) {
   Int8RowsArgs a = {};
+  a.tries = kSpinLimit;
   a.one = 1.f;
   a.x = d_x;
   a.s = reinterpret_cast<const __half*>(d_chan_scale);
@@ -590,8 +601,10 @@ cudaError_t launch_int8_encode(const void* d_x, int dtype, int64_t rows, int d,
 cudaError_t launch_rmsnorm_int8(const void* d_x, const void* d_residual, int dtype,
                                 const void* d_gain, float eps, int64_t rows, int d,
                                 const uint16_t* d_chan_scale, void* d_sum, int8_t* d_q,
-                                float* d_scale, int32_t* d_status, cudaStream_t stream) {
+                                float* d_scale, int32_t* d_status, cudaStream_t stream,
+                                unsigned tries) {
   Int8RowsArgs a = {};
+  a.tries = tries;
   a.one = 1.f;
   a.x = d_x;
   a.res = d_residual;

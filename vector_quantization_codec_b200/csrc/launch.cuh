@@ -118,10 +118,12 @@ cudaError_t launch_decode_gemv_many(const qamw_matrix* ms, int n, const uint16_t
 cudaError_t launch_int8_encode(const void* d_x, int dtype, int64_t rows, int d,
                                const uint16_t* d_chan_scale, bool divide, int8_t* d_q,
                                float* d_scale, int32_t* d_status, cudaStream_t stream);
+// tries: polls of a wait for a row's copy (kSpinLimit, but for the check of giving up).
 cudaError_t launch_rmsnorm_int8(const void* d_x, const void* d_residual, int dtype,
                                 const void* d_gain, float eps, int64_t rows, int d,
                                 const uint16_t* d_chan_scale, void* d_sum, int8_t* d_q,
-                                float* d_scale, int32_t* d_status, cudaStream_t stream);
+                                float* d_scale, int32_t* d_status, cudaStream_t stream,
+                                unsigned tries);
 // The product of up to eight tokens (called by launch_int8_gemm; three and more: d_in from 512 to 6144).
 cudaError_t launch_int8_gemv(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,

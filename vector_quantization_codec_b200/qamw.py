@@ -56,7 +56,8 @@ EXPORTS = ("qamw_row_bytes", "qamw_default_block", "qamw_bits_per_weight",
            "qamw_decode_gemv_noalloc", "qamw_polar_codebook", "qamw_encode_rows_polar",
            "qamw_scalar_codebook", "qamw_encode_rows_scalar",
            "qamw_normalised_pairs", "qamw_selftest_wait_timeout", "qamw_int8_encode_weights",
-           "qamw_int8_encode_tokens", "qamw_rmsnorm_int8", "qamw_int8_gemm")
+           "qamw_int8_encode_tokens", "qamw_rmsnorm_int8", "qamw_int8_gemm",
+           "qamw_selftest_rmsnorm_int8")
 
 
 class QamwError(RuntimeError):
@@ -111,6 +112,7 @@ def _load() -> C.CDLL:
         "qamw_int8_encode_weights": (I, [V, I, I, I, V, V, V, V, V]),
         "qamw_int8_encode_tokens": (I, [V, I, I, I, V, V, V, V, V]),
         "qamw_rmsnorm_int8": (I, [V, V, I, V, C.c_float, I, I, V, V, V, V, V, V]),
+        "qamw_selftest_rmsnorm_int8": (I, [C.c_uint, V, V, I, V, C.c_float, I, I, V, V, V, V, V, V]),
         "qamw_int8_gemm": (I, [V, V, I, V, V, I, I, V, I, V, V]),
     }
     for name, (res, args) in sig.items():
@@ -383,6 +385,17 @@ def qamw_selftest_wait_timeout(tries: int, status: torch.Tensor, cycles: torch.T
     `tries` polls and flags QAMW_STATUS_TIMEOUT in `status`."""
     _check("qamw_selftest_wait_timeout",
            _lib.qamw_selftest_wait_timeout(tries, _p(status), _p(cycles), _s(stream)))
+
+
+def qamw_selftest_rmsnorm_int8(tries: int, x: torch.Tensor, gain: torch.Tensor, sum_out: torch.Tensor | None,
+                               q: torch.Tensor, tok_scale: torch.Tensor, status: torch.Tensor,
+                               eps: float = 1e-5, residual: torch.Tensor | None = None, stream=None) -> None:
+    """qamw_rmsnorm_int8 (dense tensors of its types and shapes, on one GPU) whose waits for rows give
+    up after `tries` polls."""
+    rows, d = x.shape
+    _check("qamw_selftest_rmsnorm_int8",
+           _lib.qamw_selftest_rmsnorm_int8(tries, _p(x), _p(residual), _dtype_code(x), _p(gain), eps, rows, d,
+                                           None, _p(sum_out), _p(q), _p(tok_scale), _p(status), _s(stream)))
 
 
 def qamw_decode(m: EncodedMatrix, out: torch.Tensor | None = None,
