@@ -43,3 +43,55 @@ def test_rows_after_a_wait_that_gives_up(rows, d, residual, kind):
         st = status()
         again = qamw.qamw_rmsnorm_int8(x, gain, residual=res, status=st)
         assert st.item() == 0 and all(torch.equal(a, b) for a, b in zip(again, want))
+
+
+# ------------------------------------------------------------ data of the call ahead
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [576, 1024, 4096])
+@pytest.mark.parametrize("ntok", [300, 1000])
+def test_rows_read_what_the_call_ahead_has_just_written(ntok, d, kind):
+    """A chain in which each call reads buffers that the call ahead has just rewritten with other
+    values: a product's outputs as x of a norm, the norm's sum as the residual of the next, its
+    codes as tokens of a product."""
+    steps = 5
+    gain = (1 + 0.2 * values(1, d, kind, 3)[0].clamp(-3, 3))
+    w = [qamw.qamw_int8_encode_weights(values(d, d, kind, 20 + i, 0.1)) for i in range(steps)]
+    x0 = values(ntok, d, kind, 1)
+    y, h = torch.zeros((ntok, d), dtype=T[kind], device=DEV), torch.zeros((ntok, d), dtype=T[kind], device=DEV)
+    q = torch.zeros((ntok, d), dtype=torch.int8, device=DEV)
+    scale = torch.zeros(ntok, device=DEV)
+    out = [[torch.zeros_like(t) for t in (y, h, q, scale)] for _ in range(steps)]
+
+    def chain(wait, keep):
+        h.copy_(x0)
+        qamw.qamw_int8_encode_tokens(h, q=q, tok_scale=scale)
+        for k in range(steps):
+            wait()
+            qamw.qamw_int8_gemm(q, scale, *w[k], y=y)
+            wait()
+            qamw.qamw_rmsnorm_int8(y, gain, residual=h, sum_out=h, q=q, tok_scale=scale)
+            wait()
+            qamw.qamw_rmsnorm_int8(h, gain, residual=h, sum_out=h, q=q, tok_scale=scale)
+            if keep:
+                wait()
+                for a, b in zip(out[k], (y, h, q, scale)):
+                    a.copy_(b)
+
+    chain(torch.cuda.synchronize, True)  # nothing overlaps
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for t in (y, h, q, scale):
+            t.zero_()
+        chain(lambda: None, False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out[-1], (y, h, q, scale)))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain(lambda: None, False)
+    for _ in range(5):
+        for t in (y, h, q, scale):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out[-1], (y, h, q, scale)))

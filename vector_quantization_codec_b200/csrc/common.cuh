@@ -51,6 +51,11 @@ __device__ __forceinline__ bool mask_negative(uint64_t seed, uint32_t j) {
 // data no path kernel writes (W, x, the statistic, the codebook, the search
 // table).  pdl_trigger(), called after pdl_wait(), lets the next kernel start:
 // when kernel N starts, every kernel before N - 1 has completed.
+// The 8-bit kernels' inputs may all come from the kernel ahead, which was still
+// running when they began.  After pdl_wait() they read them by ordinary loads or
+// from L2 (__ldcg), never by the read-only path (__ldg), which takes data to be
+// constant while a kernel runs; asynchronous copies of them come behind
+// fence_proxy_async_global(), since ordinary stores may have written them.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -112,6 +117,12 @@ __device__ __forceinline__ void fwht2_lanes(float2 (&v)[32], int lanes) {
 // later asynchronous-proxy (bulk copy) accesses of the issuing thread.
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Writes to global memory that the issuing thread has seen (those of the kernel
+// ahead, after pdl_wait) are ordered before its later asynchronous-proxy accesses.
+__device__ __forceinline__ void fence_proxy_async_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
 __device__ __forceinline__ void raise_flag(int32_t* status, int flag) {

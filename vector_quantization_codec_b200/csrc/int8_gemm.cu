@@ -355,8 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_slot;
-  // every operand and scale may come from the kernel ahead (which is why the scales
-  // are not read through the read-only path)
+  // every operand and scale may come from the kernel ahead
   pdl_wait();
   pdl_trigger();
   int flags = 0;
@@ -366,8 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kCopyWarp) {
     if (elect_one()) {
-      // what the kernel ahead wrote is read by asynchronous copies from here on
-      asm volatile("fence.proxy.async.global;" ::: "memory");
+      fence_proxy_async_global();  // both operands may come from the kernel ahead
       int s = 0;
       uint32_t u = 0;
       bool ok = true;

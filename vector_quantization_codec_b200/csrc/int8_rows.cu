@@ -123,8 +123,8 @@ __device__ __forceinline__ void factors(const Int8RowsArgs& a, int vec, float2 (
     for (int i = 0; i < 4; ++i) c[i] = make_float2(1.f, 1.f);
   }
   if (a.s != nullptr) {
-    // from L2, not by the read-only path: the kernel ahead, which may have written s,
-    // was still running when this one began
+    // from L2: an ordinary load here (as good by the rule in common.cuh) was scheduled
+    // worse, 27.5 us at tokens 4001 x 13824 bf16 against 26.7
     const uint4 u = __ldcg(reinterpret_cast<const uint4*>(a.s) + vec);
     const __half2* h = reinterpret_cast<const __half2*>(&u);
     float s[8];
@@ -458,8 +458,10 @@ __global__ void __launch_bounds__(ring_threads<T, RES>(), 1)
         bulk_g2s(dst + row_bytes, static_cast<const unsigned char*>(a.res) + row * row_bytes,
                  row_bytes, &full[s]);
     };
-    if (lane == 0)
+    if (lane == 0) {
+      fence_proxy_async_global();  // x and the residual may come from the kernel ahead
       for (int j = 0; j < stages; ++j) fetch(blockIdx.x + (int64_t)j * gridDim.x, j);
+    }
     for (int64_t row = blockIdx.x, j = 0; row < a.rows; row += gridDim.x, ++j) {
       __syncthreads();
       if (gave_up[parity]) {  // this CTA's rows j .. j + stages - 1 are in flight
