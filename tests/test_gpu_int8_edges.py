@@ -95,3 +95,37 @@ def test_rows_read_what_the_call_ahead_has_just_written(ntok, d, kind):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out[-1], (y, h, q, scale)))
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_channel_scales_of_a_statistic_that_the_call_ahead_has_just_written(many):
+    """Largest magnitudes per channel from the row encoder (x transposed: one row per channel),
+    read at once by the channel scales: each step's scales are those of its own statistic."""
+    d_in, ntok, steps, bits = 4096, 8192, 4, 6
+    X = [values(d_in, ntok, "bf16", 70 + i, 1.0 + i) * (1 + torch.arange(d_in, device=DEV) % (5 + i))[:, None]
+         for i in range(steps)]
+    q, stat = torch.empty((d_in, ntok), dtype=torch.int8, device=DEV), torch.ones(d_in, device=DEV)
+    cb = torch.randn((1 << bits, 2), device=DEV)
+    W = values(64, d_in, "bf16", 5, 0.02)
+    m = qamw.EncodedMatrix.empty(64, d_in, 64, bits, cb)
+    ws = torch.empty(max(16, qamw.qamw_calibrate_many_workspace_bytes([m])), dtype=torch.uint8, device=DEV)
+
+    def scales_of(k):
+        qamw.qamw_int8_encode_tokens(X[k], q=q, tok_scale=stat)
+        if many:
+            qamw.qamw_calibrate_many([W], [m], [stat], 0.5, workspace=ws)
+            return m.chan_scale.clone()
+        return qamw.qamw_channel_scales(d_in, stat, 0.5, torch.empty(d_in, dtype=torch.float16, device=DEV))
+
+    want = []
+    for k in range(steps):
+        qamw.qamw_int8_encode_tokens(X[k], q=q, tok_scale=stat)
+        torch.cuda.synchronize()
+        r = stat.double() / stat.double().mean()
+        want.append(r.sqrt())
+    for _ in range(3):
+        got = [scales_of(k) for k in range(steps)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            # binary16 of the power: half a step, or half of the smallest step
+            assert ((g.double() - w).abs() <= w * 2.0 ** -11 * (1 + 1e-6) + 2.0 ** -25).all()

@@ -56,9 +56,14 @@ __global__ void __launch_bounds__(kScaleThreads) k_scales(const __grid_constant_
   const CalibMat& M = L.m[blockIdx.x];
   const int d_in = M.d_in;
   const float alpha = L.alpha;
+  // s may still be read by the kernel ahead, and the statistic written by it (the
+  // largest magnitudes per channel are a row encoder's scales of x transposed).  A call
+  // of 4096 channels back to back takes 6.9 us; 4.1 with the mean formed ahead of the
+  // wait, from whatever the statistic holds by then, and 5.9 with that mean checked
+  // against a second reading.
+  pdl_wait();
+  pdl_trigger();
   if (M.act == nullptr || alpha == 0.0f) {
-    pdl_wait();  // s may still be read by the kernel ahead
-    pdl_trigger();
     for (int j = threadIdx.x; j < d_in; j += kScaleThreads) M.s[j] = __float2half(1.0f);
     return;
   }
@@ -89,8 +94,6 @@ __global__ void __launch_bounds__(kScaleThreads) k_scales(const __grid_constant_
   }
   bad = __syncthreads_or(bad);
   const double mean = mean_s;
-  pdl_wait();  // s may still be read by the kernel ahead
-  pdl_trigger();
   int range = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
