@@ -3,6 +3,9 @@ before any CUDA call (made-up addresses, no GPU touched), the Python wrappers
 refuse tensors that do not fit, and the plain forms the GPU tests compare with
 agree with the 64-bit mathematics."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -114,3 +117,18 @@ def test_gemm_c_types_take_null():
 def test_giving_up_check_argument_errors(tries, st, eps, rc):
     assert L.qamw_selftest_rmsnorm_int8(tries, FAKE, FAKE, BF16, FAKE, eps, 4, 128, None, FAKE, FAKE, FAKE,
                                         st, None) == rc
+
+
+@pytest.mark.parametrize("shape", [(65536, 1 << 30, 32768), (65536, 1 << 30, 64), (1, 1 << 30, 64),
+                                   (65536, 1, 32768), (12000, 1 << 30, 32768)], ids=str)
+def test_products_of_the_largest_sizes_get_a_plan(shape):
+    """The largest sizes that the call allows are planned (and then fail to launch: the child sees no
+    GPU), whatever their estimated time."""
+    ntok, d_out, d_in = shape
+    code = ("from vector_quantization_codec_b200 import qamw\n"
+            f"rc = qamw.lib().qamw_int8_gemm({FAKE}, {FAKE}, {ntok}, {FAKE}, {FAKE}, {d_out}, {d_in}, {FAKE}, "
+            f"{BF16}, None, None)\nassert rc == {qamw.QAMW_ERR_CUDA}, rc\n")
+    r = subprocess.run([sys.executable, "-c", code], env={**os.environ, "CUDA_VISIBLE_DEVICES": ""},
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr)

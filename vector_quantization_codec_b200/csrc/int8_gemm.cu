@@ -17,7 +17,7 @@
 // -> 4096 14.3 us, where the weights' way from HBM takes 7 and the cluster's
 // partial sums 2.5; 16 tokens 4096 -> 11008 11.1 us (4.1 TB/s).
 #include <algorithm>
-#include <climits>
+#include <cstdint>
 #include <type_traits>
 
 #include "common.cuh"
@@ -670,7 +670,7 @@ struct Int8Plan {
 // tokens) and a floor; the last tile's epilogue is not hidden, earlier ones are
 // unless the depth is short; sharing a tile's chunks among CTAs costs two
 // cluster barriers and the reading of the partial sums.
-int plan_ns(int ntok, int d_out, int chunks, int cg, int nt, int splits, int sms) {
+int64_t plan_ns(int ntok, int d_out, int chunks, int cg, int nt, int splits, int sms) {
   const int64_t tiles =
       (int64_t)((d_out + kRowsM * cg - 1) / (kRowsM * cg)) * ((ntok + nt - 1) / nt);
   const int at_once = std::max(1, sms / (cg * splits));
@@ -679,14 +679,14 @@ int plan_ns(int ntok, int d_out, int chunks, int cg, int nt, int splits, int sms
   const int main = (chunks + splits - 1) / splits * chunk, epilogue = 10 * nt;
   int64_t t = waves * (std::max(main, epilogue) + 1900) + epilogue;
   if (splits > 1) t += waves * 2150 + (waves - 1) * epilogue + 7 * nt;
-  return (int)std::min<int64_t>(t, INT_MAX);
+  return t;
 }
 
 // bf16_rows: bf16 outputs whose rows are multiples of 16 bytes.
 Int8Plan plan_int8(int ntok, int d_out, int d_in, bool bf16_rows) {
   Int8Plan p = {};
   const int chunks = (d_in + kChunk - 1) / kChunk, sms = sm_count();
-  int best = INT_MAX;
+  int64_t best = INT64_MAX;
   for (int cg = 1; cg <= 2; ++cg) {
     // tokens in steps of 16 per CTA; single CTAs only where a pair's tile would be
     // wider than the batch needs
@@ -696,7 +696,7 @@ Int8Plan plan_int8(int ntok, int d_out, int d_in, bool bf16_rows) {
       for (int splits = 1; splits * cg <= kMaxSplits; ++splits) {
         if (splits > 1 && 2 * splits > chunks) break;
         if (splits * cg == 5 || splits * cg == 7) continue;  // leave SMs of a GPC unused
-        const int t = plan_ns(ntok, d_out, chunks, cg, nt, splits, sms);
+        const int64_t t = plan_ns(ntok, d_out, chunks, cg, nt, splits, sms);
         if (t < best) {
           best = t;
           p.cg = cg;
