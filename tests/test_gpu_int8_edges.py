@@ -129,3 +129,42 @@ def test_channel_scales_of_a_statistic_that_the_call_ahead_has_just_written(many
         for g, w in zip(got, want):
             # binary16 of the power: half a step, or half of the smallest step
             assert ((g.double() - w).abs() <= w * 2.0 ** -11 * (1 + 1e-6) + 2.0 ** -25).all()
+
+
+# ------------------------------------------------------------ ends of the range
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 512, 2048, 8192, 13312, 28672, 32768])
+def test_norm_of_rows_whose_squares_overflow(d, kind):
+    """Rows of up to the type's largest value, whose sum of squares leaves binary32 by little or by
+    far, with factors that bring the values back into range or near its other end."""
+    largest = torch.finfo(T[kind]).max
+    g = torch.Generator().manual_seed(d)
+    u = torch.rand((6, d), generator=g) * 0.5 + 0.5
+    u[:, ::3] *= -1
+    rows = torch.stack([torch.full((d,), largest), u[0] * largest, u[1] * 3e38, u[2] * 1.5e38, u[3] * 2e19,
+                        u[4] * 1e25, torch.where(torch.arange(d) == d // 2, 1e20, 1e-3)])
+    x = rows.to(T[kind]).to(DEV)
+    eps = 1e-5
+    for factor, sc in ((1.0, None), (2.0 ** -60, 2.0 ** 4), (2.0 ** -100, 2.0 ** 14)):
+        gain = torch.full((d,), factor, dtype=T[kind], device=DEV)
+        s = None if sc is None else torch.full((d,), sc, dtype=torch.float16, device=DEV)
+        sn = None if s is None else s.cpu().numpy()
+        c = ref.factors32(d, sn, gain.float().cpu().numpy())
+        xn = x.float().cpu().numpy()
+        q_want, _, a = ref.rows32(xn, c)
+        _, scale64 = ref.rows64(xn, sn, gain.float().cpu().numpy(), True, eps)
+        many = x.repeat(50, 1)  # more rows than are taken one per CTA
+        for got in (qamw.qamw_rmsnorm_int8(x, gain, eps, chan_scale=s),
+                    qamw.qamw_rmsnorm_int8(x, gain, eps, residual=torch.zeros_like(x), chan_scale=s)[1:],
+                    qamw.qamw_rmsnorm_int8(many, gain, eps, chan_scale=s),
+                    qamw.qamw_rmsnorm_int8(many, gain, eps, residual=torch.zeros_like(many), chan_scale=s)[1:]):
+            n = len(got[1]) // len(x)
+            np.testing.assert_array_equal(got[0].cpu().numpy(), np.tile(q_want, (n, 1)))
+            # v, a and a / 127: 3 roundings.  1 / rms: a sum of positive terms, each off by at most
+            # one rounding per addition on its path (2 per 64 columns of a lane, 5 in the shuffles)
+            # and the squares by one, halved by the root; then at most five more, and half of the
+            # smallest step where the scale is that small
+            tol = (3 + (2 * d / 64 + 5 + 1) / 2 + 5) * ref.U32
+            want = np.tile(scale64 * (a >= ref.TINY), n)
+            assert (np.abs(got[1].cpu().numpy() - want) <= tol * want + 2.0 ** -150).all()

@@ -226,9 +226,12 @@ __device__ __forceinline__ RowOut row_out(uint32_t top) {
 }
 
 // The row's scale, by its first warp.  Squares that overflow (|h| beyond about
-// 2^56) are summed again with h 2^-70 from memory, by the warp alone: h is x, or
+// 2^56) are summed again with h 2^-80 from memory, by the warp alone: h is x, or
 // the sum that the row's threads have written ahead of the reduction's barrier.
-constexpr float kDown = 8.470329472543003e-22f;  // 2^-70
+// 2^15 squares of 2^(128 - 80) stay below 2^111, and a sum that overflowed is
+// above 2^-32 then; scale and factor are joined in 64 bits, since scale 2^-80 and
+// 1 / rms alone may both leave the normal range.
+constexpr float kDown = 8.271806125530277e-25f;  // 2^-80
 template <typename T, bool NORM>
 __device__ __forceinline__ void put_scale(const Int8RowsArgs& a, int64_t row, uint32_t top, bool some,
                                           float sum, int lane, int& flags) {
@@ -247,7 +250,7 @@ __device__ __forceinline__ void put_scale(const Int8RowsArgs& a, int64_t row, ui
           w = fma2(f, f, w);
         }
       }
-      scale = scale * kDown * (1.f / sqrtf(warp_sum(w.x + w.y) / (float)a.d));
+      scale = (float)((double)scale * kDown / sqrt((double)warp_sum(w.x + w.y) / a.d));
     } else {
       scale *= 1.f / sqrtf(sum / (float)a.d + a.eps);
     }
