@@ -1,5 +1,9 @@
 """The 8-bit (W8A8) operators where they are easily wrong: waits that give up, buffers that the
 call ahead has just written, the ends of the range, first calls from several host threads."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -168,3 +172,60 @@ def test_norm_of_rows_whose_squares_overflow(d, kind):
             tol = (3 + (2 * d / 64 + 5 + 1) / 2 + 5) * ref.U32
             want = np.tile(scale64 * (a >= ref.TINY), n)
             assert (np.abs(got[1].cpu().numpy() - want) <= tol * want + 2.0 ** -150).all()
+
+
+# ------------------------------------------------------------ several host threads
+
+FIRST_CALLS = """
+import threading
+import torch
+from vector_quantization_codec_b200 import qamw
+
+torch.manual_seed(0)
+dev = "cuda"
+ints = lambda r, d: torch.randint(-127, 128, (r, d), dtype=torch.int8, device=dev)
+jobs = []  # per kernel, calls that need shared memory of different sizes, above 48 KB all
+for t in (torch.bfloat16, torch.float32):
+    for ntok in (1, 2):
+        jobs.append([lambda a=(ints(ntok, d), torch.ones(ntok, device=dev), ints(64, d), torch.ones(64, device=dev)),
+                     t=t: (qamw.qamw_int8_gemm(*a, dtype=t),) for d in (32768, 28672, 24576, 20480)])
+    for norm in (False, True):
+        for d in ((16448, 20480, 24576, 32768), (11008, 10240, 9216, 8192)):
+            jobs.append([lambda x=torch.randn((400, w), device=dev).to(t), g=torch.ones(w, device=dev).to(t), norm=norm:
+                         qamw.qamw_rmsnorm_int8(x, g) if norm else qamw.qamw_int8_encode_tokens(x) for w in d])
+streams = [torch.cuda.Stream() for _ in range(8)]
+torch.cuda.synchronize()
+bad = []
+for job in jobs:
+    first, gate = {}, threading.Barrier(2 * len(job))
+    def call(i):
+        with torch.cuda.stream(streams[i]):
+            gate.wait()
+            try:
+                first[i] = job[i % len(job)]()
+            except qamw.QamwError as e:
+                bad.append(str(e))
+    threads = [threading.Thread(target=call, args=(i,)) for i in range(2 * len(job))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for i in range(2 * len(job)):
+        try:
+            again = job[i % len(job)]()
+        except qamw.QamwError as e:
+            bad.append(str(e))
+            continue
+        torch.cuda.synchronize()
+        if i in first and not all(torch.equal(a, b) for a, b in zip(first[i], again)):
+            bad.append("results differ")
+assert not bad, bad
+"""
+
+
+def test_first_calls_of_several_host_threads():
+    """Threads that make a kernel's first calls at the same time, with sizes that need different
+    amounts of shared memory: none is refused, then or later, and all give the same results again."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for _ in range(3):  # a new process each: what a call sets up lives as long as it
+        r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-2000:]

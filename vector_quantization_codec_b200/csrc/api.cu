@@ -85,28 +85,22 @@ int persistent_grid(const void* kernel, int threads, size_t smem, int64_t work_c
   return (int)(g < 1 ? 1 : g);
 }
 
+// The attribute is an overwrite, not a maximum, so a kernel gets the most that its
+// device allows, once, whatever this call needs: calls of several host threads with
+// other sizes cannot lower it.  (A launch reserves what it asks for, not this.)
 cudaError_t allow_smem(const void* kernel, size_t smem) {
   if (smem <= 48 * 1024) return cudaSuccess;
-  // the attribute is a maximum: one call with the largest size seen so far
   const LaunchKey k{current_device(), kernel, 0, 0};
-  int have = 0;
-  if (cache_get(g_smem_optin, k, &have) && (size_t)have >= smem) return cudaSuccess;
-  const cudaError_t err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (err == cudaSuccess) {
-    std::lock_guard<std::mutex> lock(g_smem_optin.mu);
-    bool found = false;
-    for (int i = 0; i < g_smem_optin.n; ++i)
-      if (g_smem_optin.key[i] == k) {
-        if (g_smem_optin.value[i] < (int)smem) g_smem_optin.value[i] = (int)smem;
-        found = true;
-      }
-    if (!found && g_smem_optin.n < 256) {
-      g_smem_optin.key[g_smem_optin.n] = k;
-      g_smem_optin.value[g_smem_optin.n] = (int)smem;
-      ++g_smem_optin.n;
-    }
-  }
+  int done = 0;
+  if (cache_get(g_smem_optin, k, &done)) return cudaSuccess;
+  int most = 0;
+  cudaFuncAttributes attr;
+  cudaError_t err = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, k.dev);
+  if (err == cudaSuccess) err = cudaFuncGetAttributes(&attr, kernel);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               most - (int)attr.sharedSizeBytes);
+  if (err == cudaSuccess) cache_put(g_smem_optin, k, 1);
   return err;
 }
 
