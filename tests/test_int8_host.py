@@ -132,3 +132,48 @@ def test_products_of_the_largest_sizes_get_a_plan(shape):
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                        capture_output=True, text=True)
     assert r.returncode == 0, (r.returncode, r.stderr)
+
+
+CACHE_MAIN = r"""
+#include <cstdio>
+#include <thread>
+#include <vector>
+#include "launch_cache.h"
+using namespace qamw;
+int main() {
+  static LaunchCache cache;
+  static char kernels[8];
+  // every width of every kernel, as several threads meet them in different orders
+  const auto key = [](int i) {
+    return LaunchKey{i % 2, &kernels[i % 8], 32 * (1 + i % 32), (size_t)(64 * (i / 8))};
+  };
+  const int n = 4096;
+  std::vector<std::thread> threads;
+  for (int t = 0; t < 4; ++t)
+    threads.emplace_back([&, t] {
+      for (int i = 0; i < n; ++i) {
+        const int j = (i * 7 + t * 1000) % n;
+        int v;
+        if (!cache.get(key(j), &v)) cache.put(key(j), j);
+      }
+    });
+  for (auto& t : threads) t.join();
+  for (int i = 0; i < n; ++i) {
+    int v = -1;
+    if (!cache.get(key(i), &v) || v != i) return printf("key %d: %d\n", i, v), 1;
+  }
+  int v;
+  return cache.get(LaunchKey{2, kernels, 32, 0}, &v) ? 2 : 0;
+}
+"""
+
+
+def test_launch_facts_of_every_width_are_kept(tmp_path):
+    """What a call looks up once per kernel and width stays looked up, however many there are."""
+    src, exe = tmp_path / "main.cpp", tmp_path / "main"
+    src.write_text(CACHE_MAIN)
+    csrc = os.path.join(os.path.dirname(os.path.abspath(qamw.__file__)), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-pthread", "-I", csrc, str(src), "-o", str(exe)],
+                   check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stdout)

@@ -3,10 +3,10 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdio>
-#include <mutex>
 
 #include "common.cuh"
 #include "launch.cuh"
+#include "launch_cache.h"
 
 namespace qamw {
 
@@ -25,43 +25,7 @@ int sm_count() {
 // Occupancy and shared-memory opt-in are per (device, kernel, shape) facts:
 // computed once and cached, so that a call costs the launches and little else.
 namespace {
-struct LaunchKey {
-  int dev;
-  const void* fn;
-  int threads;
-  size_t smem;
-  bool operator==(const LaunchKey& o) const {
-    return dev == o.dev && fn == o.fn && threads == o.threads && smem == o.smem;
-  }
-};
-struct LaunchCache {
-  std::mutex mu;
-  LaunchKey key[256];
-  int value[256];
-  int n = 0;
-};
 LaunchCache g_occupancy, g_smem_optin;
-
-bool cache_get(LaunchCache& c, const LaunchKey& k, int* v) {
-  std::lock_guard<std::mutex> lock(c.mu);
-  for (int i = 0; i < c.n; ++i)
-    if (c.key[i] == k) {
-      *v = c.value[i];
-      return true;
-    }
-  return false;
-}
-
-void cache_put(LaunchCache& c, const LaunchKey& k, int v) {
-  std::lock_guard<std::mutex> lock(c.mu);
-  for (int i = 0; i < c.n; ++i)
-    if (c.key[i] == k) return;
-  if (c.n < 256) {
-    c.key[c.n] = k;
-    c.value[c.n] = v;
-    ++c.n;
-  }
-}
 
 int current_device() {
   int dev = 0;
@@ -73,12 +37,12 @@ int current_device() {
 int persistent_grid(const void* kernel, int threads, size_t smem, int64_t work_ctas) {
   const LaunchKey k{current_device(), kernel, threads, smem};
   int per_sm = 0;
-  if (!cache_get(g_occupancy, k, &per_sm)) {
+  if (!g_occupancy.get(k, &per_sm)) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) !=
             cudaSuccess ||
         per_sm < 1)
       per_sm = 1;
-    cache_put(g_occupancy, k, per_sm);
+    g_occupancy.put(k, per_sm);
   }
   const int64_t resident = (int64_t)per_sm * sm_count();
   int64_t g = work_ctas < resident ? work_ctas : resident;
@@ -92,7 +56,7 @@ cudaError_t allow_smem(const void* kernel, size_t smem) {
   if (smem <= 48 * 1024) return cudaSuccess;
   const LaunchKey k{current_device(), kernel, 0, 0};
   int done = 0;
-  if (cache_get(g_smem_optin, k, &done)) return cudaSuccess;
+  if (g_smem_optin.get(k, &done)) return cudaSuccess;
   int most = 0;
   cudaFuncAttributes attr;
   cudaError_t err = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, k.dev);
@@ -100,7 +64,7 @@ cudaError_t allow_smem(const void* kernel, size_t smem) {
   if (err == cudaSuccess)
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                most - (int)attr.sharedSizeBytes);
-  if (err == cudaSuccess) cache_put(g_smem_optin, k, 1);
+  if (err == cudaSuccess) g_smem_optin.put(k, 1);
   return err;
 }
 
