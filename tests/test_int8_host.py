@@ -177,3 +177,25 @@ def test_launch_facts_of_every_width_are_kept(tmp_path):
                    check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, (r.returncode, r.stdout)
+
+
+def test_a_refused_stream_leaves_the_device_as_it_was(monkeypatch):
+    """The wrappers make the tensors' device current before they look at the stream: an argument that
+    is no stream must not leave it so."""
+    entered = []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append(self.index)
+
+        def __exit__(self, *exc):
+            entered.pop()
+
+    monkeypatch.setattr(qamw.torch.cuda, "device", Device)
+    for stream in ("no stream", object(), [1]):
+        with pytest.raises((TypeError, ValueError)):
+            qamw._enter(3, stream)
+        assert not entered

@@ -546,17 +546,16 @@ def _enter(index: int, stream):
     context to close."""
     if stream is None and _current_device() == index:
         return None
-    ctx = contextlib.ExitStack()
-    ctx.enter_context(torch.cuda.device(index))
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = (torch.cuda.ExternalStream(int(stream), device=index) if int(stream)
-                      else torch.cuda.default_stream(index))
-        if stream.device.index != index:
-            ctx.close()
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
-        ctx.enter_context(torch.cuda.stream(stream))
-    return ctx
+    with contextlib.ExitStack() as ctx:
+        ctx.enter_context(torch.cuda.device(index))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = (torch.cuda.ExternalStream(int(stream), device=index) if int(stream)
+                          else torch.cuda.default_stream(index))
+            if stream.device.index != index:
+                raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+            ctx.enter_context(torch.cuda.stream(stream))
+        return ctx.pop_all()  # kept open: what raises above closes it
 
 
 def _used_on(index: int, *tensors) -> None:
