@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from tests import int8_ref as ref
-from tests.test_gpu_int8 import DEV, T, status, values
+from tests.test_gpu_int8 import DEV, T, check_gemm, ints, scales, status, values
 from vector_quantization_codec_b200 import qamw
 
 pytestmark = pytest.mark.gpu
@@ -229,3 +229,20 @@ def test_first_calls_of_several_host_threads():
     for _ in range(3):  # a new process each: what a call sets up lives as long as it
         r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True)
         assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------ kernels of a few tokens
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d_out,d_in", [(7104, 1024), (7105, 1024), (7200, 256), (7201, 448), (9003, 512), (7105, 2048),
+                                        (7300, 2112), (4736, 4160), (4737, 4160), (8192, 4160), (11008, 5376),
+                                        (11001, 5440), (3552, 6144), (3553, 6144), (3552, 32768), (3553, 32768),
+                                        (5000, 26048), (65, 5632)])
+def test_products_of_a_few_tokens_on_both_sides_of_each_rule(d_out, d_in, kind):
+    """One to nine tokens where the choice of a kernel changes with the number of rows and their
+    length: the exact sums, and a token's outputs the same bit for bit whatever comes with it."""
+    x, w, xs, ws = ints(9, d_in, 1, full=True), ints(d_out, d_in, 2, full=True), scales(9, 3), scales(d_out, 4)
+    want = check_gemm(x, xs, w, ws, T[kind])
+    for ntok in (1, 2, 3, 5, 8):
+        got = check_gemm(x[:ntok].contiguous(), xs[:ntok].contiguous(), w, ws, T[kind])
+        assert torch.equal(got, want[:ntok])

@@ -715,6 +715,45 @@ Int8Plan plan_int8(int ntok, int d_out, int d_in, bool bf16_rows) {
   return p;
 }
 
+// A few tokens: the weights' rows straight from global memory, by dot products (a
+// warp a row, 32 rows of an SM at once) or by the warp-level MMA (a CTA 16 rows, 48
+// of an SM at once), or else the tensor-core kernel of this file.  Measured, us,
+// dot / MMA / tensor core (back to back over weights larger than L2 where they are):
+//   1 token   4096 -> 4096   3.8 / 6.1 / 7.3     4096 -> 32001 19.3 / 21.6 / 23.0
+//   2 tokens  4096 -> 4096   4.8 / 6.2 / 7.4     4096 -> 32001 21.1 / 21.9 / 23.1
+// Rows shorter than a warp's 4 KB leave loads empty, which shows where a warp takes
+// several rows:
+//   1 token   1024 -> 6000   3.4 / 3.9 / 4.2     1024 -> 13824  5.7 / 4.4 / 6.2
+//   1 token    256 -> 4096   2.7 / 3.3 / 3.1      256 -> 32001 10.4 / 4.9 / 5.1
+//   2 tokens  2048 -> 4096   3.7 / 4.2 / 5.4     2048 -> 13824  7.5 / 6.6 / 8.4
+// and so do rows that are a little longer, with two tokens:
+//   2 tokens  5120 -> 4096   6.5 / 7.4 / 8.3     5120 -> 13824 14.9 / 13.6 / 14.4
+//   2 tokens  5632 -> 11008 13.7 / 14.5 / 14.1   5376 -> 11008 13.9 / 13.5 / 14.0
+// Two long tokens leave no room for four CTAs of the dot products on an SM:
+//   2 tokens 20480 -> 4096  15.7 / - / 16.9     32768 -> 4096  38.0 / - / 25.7
+//   2 tokens 32768 -> 2048  20.1 / - / 22.3     32768 -> 13824 83.2 / - / 85.2
+// The MMA takes too many steps per 16 rows where d_in is large, and a round of rows
+// that fills few SMs costs as much as a full one:
+//   5 tokens  4096 -> 8192   -   / 9.2 / 9.4     5120 -> 8192   -   / 12.1 / 10.7
+//   5 tokens  5120 -> 11008  -  / 13.2 / 13.3    5632 -> 11008  -   / 14.7 / 14.2
+//   5 tokens  5632 -> 2048   -   / 6.3 / 12.1    8192 -> 1024   -   / 7.4 / 6.1
+enum class FewTokens { kNone, kDot, kMma };
+
+FewTokens few_token_kernel(int ntok, int d_out, int d_in) {
+  if (ntok > 8 || d_in < 256) return FewTokens::kNone;
+  const int64_t sms = sm_count(), groups = ((int64_t)d_out + 15) / 16, at_once = 3 * sms;
+  // one round of 16 rows per CTA, or a last round that is not almost empty
+  const bool full = groups <= at_once || 4 * groups >= 3 * ((groups + at_once - 1) / at_once * at_once);
+  const bool mma_fits = d_in >= 512 && (d_in <= 4096 || (d_in <= 5376 && full) ||
+                                        (d_in <= 6144 && d_out <= 24 * sms));
+  const FewTokens mma = mma_fits ? FewTokens::kMma : FewTokens::kNone;
+  if (ntok > 2) return mma;
+  if (d_in <= 1024 * ntok && d_out > 48 * sms) return mma;
+  if (ntok == 2 && d_in > 4096 && d_in <= 5376 && d_out > 32 * sms && full) return mma;
+  if (ntok == 2 && d_in > 26000 && d_out > 24 * sms) return FewTokens::kNone;
+  return FewTokens::kDot;
+}
+
 template <int CG, typename T>
 cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap& mx,
                      const CUtensorMap& my, const Int8GemmArgs& a, cudaStream_t stream) {
@@ -749,16 +788,10 @@ cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap
 cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
                              int32_t* d_status, cudaStream_t stream) {
-  // A few tokens: the weights' rows straight from global memory.  Measured against
-  // the kernel below, us: 1 token 4096 -> 4096 3.8 (7.7), 4096 -> 32001 18.8 (23.1);
-  // 2 tokens 4.7 (7.8), 20.7 (23.3), 5120 -> 13824 15.2 (14.3); 5 tokens 4096 -> 4096
-  // 6.3 (7.3), 4096 -> 11008 10.4 (11.5), 4096 -> 32001 22.0 (23.2), 2048 -> 64 2.3
-  // (4.2).  Short rows leave lanes idle (1 token 64 -> 50000 15.2 against 4.9; 8
-  // tokens 256 -> 5632 3.4 against 3.0); with three tokens and more long ones take too
-  // many steps, and too much shared memory, per 16 rows (5 tokens 8192 -> 1024 6.5
-  // against 5.7, 11008 -> 4096 12.5 against 11.8).
-  if ((ntok <= 2 && d_in >= 256) || (ntok <= 8 && d_in >= 512 && d_in <= 6144))
-    return launch_int8_gemv(d_x, d_x_scale, ntok, d_w, d_w_scale, d_out, d_in, d_y, dtype, stream);
+  const FewTokens few = few_token_kernel(ntok, d_out, d_in);
+  if (few != FewTokens::kNone)
+    return launch_int8_gemv(d_x, d_x_scale, ntok, d_w, d_w_scale, d_out, d_in, d_y, dtype,
+                            few == FewTokens::kMma, stream);
   const Int8Plan p = plan_int8(ntok, d_out, d_in,
                                dtype == QAMW_DTYPE_BF16 && d_out % 8 == 0 &&
                                    (reinterpret_cast<uintptr_t>(d_y) & 15u) == 0);

@@ -255,19 +255,18 @@ cudaError_t run_gemv_mma(const Int8GemvArgs& a, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t run_any(const Int8GemvArgs& a, cudaStream_t stream) {
-  if (a.ntok == 1) return run_gemv<1, T>(a, stream);
-  if (a.ntok == 2) return run_gemv<2, T>(a, stream);
-  return run_gemv_mma<T>(a, stream);
+cudaError_t run_any(const Int8GemvArgs& a, bool mma, cudaStream_t stream) {
+  if (mma) return run_gemv_mma<T>(a, stream);
+  return a.ntok == 1 ? run_gemv<1, T>(a, stream) : run_gemv<2, T>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_int8_gemv(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
-                             cudaStream_t stream) {
+                             bool mma, cudaStream_t stream) {
   const Int8GemvArgs a = {d_x, d_x_scale, d_w, d_w_scale, d_y, ntok, d_out, d_in, 1};
-  return dtype == QAMW_DTYPE_F32 ? run_any<float>(a, stream) : run_any<__nv_bfloat16>(a, stream);
+  return dtype == QAMW_DTYPE_F32 ? run_any<float>(a, mma, stream) : run_any<__nv_bfloat16>(a, mma, stream);
 }
 
 }  // namespace qamw

@@ -124,10 +124,11 @@ cudaError_t launch_rmsnorm_int8(const void* d_x, const void* d_residual, int dty
                                 const uint16_t* d_chan_scale, void* d_sum, int8_t* d_q,
                                 float* d_scale, int32_t* d_status, cudaStream_t stream,
                                 unsigned tries);
-// The product of up to eight tokens (called by launch_int8_gemm; three and more: d_in from 512 to 6144).
+// The product of one or two tokens by dot products, or of up to eight by the warp-level MMA
+// (called by launch_int8_gemm, which chooses).
 cudaError_t launch_int8_gemv(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
-                             cudaStream_t stream);
+                             bool mma, cudaStream_t stream);
 cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
                              int32_t* d_status, cudaStream_t stream);
