@@ -42,7 +42,8 @@ __device__ __forceinline__ int dot16(uint4 a, uint4 b, int acc) {
 constexpr int kAhead = 8;
 template <int NTOK, typename T>
 __global__ void __launch_bounds__(kGemvWarps * 32, 4) k_int8_gemv(const Int8GemvArgs a) {
-  // [NTOK][d_in / 16], and room for the reads past the end (which meet zeros of W)
+  // [NTOK][d_in / 16], the last token's row up to a whole step (reads past the end
+  // meet zeros of W)
   extern __shared__ __align__(16) uint4 xv[];
   __shared__ int part[2][kGemvWarps][NTOK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -126,7 +127,9 @@ cudaError_t run_gemv(Int8GemvArgs a, cudaStream_t stream) {
   while (a.per_row < kGemvWarps && (int64_t)a.d_out * a.per_row < 24 * sm_count() &&
          a.per_row * 2 * 512 <= a.d_in)
     a.per_row *= 2;
-  const size_t smem = (size_t)NTOK * a.d_in + (size_t)kAhead * 512 * a.per_row;
+  // the last token's reads end with its last whole step of kAhead pieces per warp
+  const size_t step = (size_t)kAhead * 512 * a.per_row;
+  const size_t smem = (size_t)(NTOK - 1) * a.d_in + (a.d_in + step - 1) / step * step;
   cudaError_t err = allow_smem(p, smem + kGemvStatic);
   if (err != cudaSuccess) return err;
   const int rows_cta = kGemvWarps / a.per_row;
