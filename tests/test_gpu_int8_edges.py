@@ -246,3 +246,12 @@ def test_products_of_a_few_tokens_on_both_sides_of_each_rule(d_out, d_in, kind):
     for ntok in (1, 2, 3, 5, 8):
         got = check_gemm(x[:ntok].contiguous(), xs[:ntok].contiguous(), w, ws, T[kind])
         assert torch.equal(got, want[:ntok])
+
+
+@pytest.mark.parametrize("ntok,d_out,d_in", [(9, 2048, 4096), (16, 2047, 8192), (32, 2048, 2048), (12, 1900, 20480),
+                                             (64, 2500, 8192), (40, 1000, 4096), (16, 4700, 11008)])
+def test_products_whose_depth_clusters_share(ntok, d_out, d_in):
+    """Few tiles: clusters of two to eight CTAs share a tile's depth, in one wave or more."""
+    for kind in ("bf16", "f32"):
+        check_gemm(ints(ntok, d_in, 1, full=True), scales(ntok, 2), ints(d_out, d_in, 3, full=True),
+                   scales(d_out, 4), T[kind])

@@ -17,6 +17,7 @@
 // -> 4096 14.3 us, where the weights' way from HBM takes 7 and the cluster's
 // partial sums 2.5; 16 tokens 4096 -> 11008 11.1 us (4.1 TB/s).
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -663,17 +664,48 @@ struct Int8Plan {
   bool staged;
 };
 
-// Estimated time (ns) of a plan, fitted to 360 measured (shape, plan) pairs from
-// 1 x 512 -> 1000 to 3000 x 4096 -> 11008; over those 26 shapes the plan that it
-// picks is within 4% of the fastest one measured (mean 0.3%).  A chunk of a CTA costs the
-// longest of its MMAs, its way through shared memory (128 channels and nt / cg
-// tokens) and a floor; the last tile's epilogue is not hidden, earlier ones are
-// unless the depth is short; sharing a tile's chunks among CTAs costs two
-// cluster barriers and the reading of the partial sums.
-int64_t plan_ns(int ntok, int d_out, int chunks, int cg, int nt, int splits, int sms) {
+// Clusters of `per` CTAs of k_int8_gemm that the current device holds at once.  A
+// cluster's CTAs share a GPC, whose SMs are rarely a multiple of four or eight: a
+// B200 of 148 SMs holds 45, 33, 22 and 15 of three, four, six and eight CTAs.  (By
+// SMs / 8 = 18 the estimate below took 16 clusters of eight for one wave: 16 tokens
+// 4096 -> 2048 took 9.6 us in two, and takes 5.7 with six CTAs a cluster.)
+int clusters_at_once(int per) {
+  static std::atomic<int> cached[64][kMaxSplits + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return std::max(1, sm_count() / per);
+  int n = cached[dev][per].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  // registers, shared memory and threads of a CTA are alike in all four instances
+  auto fn = &k_int8_gemm<1, float>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)per);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemAll;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)per;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (per == 1 || allow_smem(reinterpret_cast<const void*>(fn), kSmemAll) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1)
+    n = std::max(1, sm_count() / per);
+  cached[dev][per].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Estimated time (ns) of a plan, fitted to 360 measured (shape, plan) pairs.  Over
+// 28 shapes from 9 x 4096 -> 4096 to 8192 x 4096 -> 11008, with 750 plans measured on
+// the kernel as it is, the plan that it picks is within 6% of the fastest (mean 1%),
+// but for 16 x 4096 -> 2048 (10%: six CTAs a cluster, not four).  A chunk of a CTA
+// costs the longest of its MMAs, its way through shared memory (128 channels and nt /
+// cg tokens) and a floor; the last tile's epilogue is not hidden, earlier ones are
+// unless the depth is short; sharing a tile's chunks among CTAs costs two cluster
+// barriers and the reading of the partial sums.
+int64_t plan_ns(int ntok, int d_out, int chunks, int cg, int nt, int splits, int at_once) {
   const int64_t tiles =
       (int64_t)((d_out + kRowsM * cg - 1) / (kRowsM * cg)) * ((ntok + nt - 1) / nt);
-  const int at_once = std::max(1, sms / (cg * splits));
   const int64_t waves = (tiles + at_once - 1) / at_once;
   const int chunk = std::max(std::max(118 * nt / 100, 98 * (kRowsM + nt / cg) / 100), 225);
   const int main = (chunks + splits - 1) / splits * chunk, epilogue = 10 * nt;
@@ -685,8 +717,10 @@ int64_t plan_ns(int ntok, int d_out, int chunks, int cg, int nt, int splits, int
 // bf16_rows: bf16 outputs whose rows are multiples of 16 bytes.
 Int8Plan plan_int8(int ntok, int d_out, int d_in, bool bf16_rows) {
   Int8Plan p = {};
-  const int chunks = (d_in + kChunk - 1) / kChunk, sms = sm_count();
+  const int chunks = (d_in + kChunk - 1) / kChunk;
   int64_t best = INT64_MAX;
+  int at_once[kMaxSplits + 1];
+  for (int per = 1; per <= kMaxSplits; ++per) at_once[per] = clusters_at_once(per);
   for (int cg = 1; cg <= 2; ++cg) {
     // tokens in steps of 16 per CTA; single CTAs only where a pair's tile would be
     // wider than the batch needs
@@ -696,7 +730,7 @@ Int8Plan plan_int8(int ntok, int d_out, int d_in, bool bf16_rows) {
       for (int splits = 1; splits * cg <= kMaxSplits; ++splits) {
         if (splits > 1 && 2 * splits > chunks) break;
         if (splits * cg == 5 || splits * cg == 7) continue;  // leave SMs of a GPC unused
-        const int64_t t = plan_ns(ntok, d_out, chunks, cg, nt, splits, sms);
+        const int64_t t = plan_ns(ntok, d_out, chunks, cg, nt, splits, at_once[cg * splits]);
         if (t < best) {
           best = t;
           p.cg = cg;
@@ -736,7 +770,7 @@ Int8Plan plan_int8(int ntok, int d_out, int d_in, bool bf16_rows) {
 // that fills few SMs costs as much as a full one:
 //   5 tokens  4096 -> 8192   -   / 9.2 / 9.4     5120 -> 8192   -   / 12.1 / 10.7
 //   5 tokens  5120 -> 11008  -  / 13.2 / 13.3    5632 -> 11008  -   / 14.7 / 14.2
-//   5 tokens  5632 -> 2048   -   / 6.3 / 12.1    8192 -> 1024   -   / 7.4 / 6.1
+//   5 tokens  5632 -> 2048   -   / 6.3 / 6.9     8192 -> 1024   -   / 7.4 / 6.1
 enum class FewTokens { kNone, kDot, kMma };
 
 FewTokens few_token_kernel(int ntok, int d_out, int d_in) {
