@@ -160,6 +160,16 @@ QAMW_API int qamw_selftest_rmsnorm_int8(unsigned tries, const void *d_x, const v
                                         const uint16_t *d_chan_scale, void *d_sum, int8_t *d_q,
                                         float *d_tok_scale, int32_t *d_status, void *stream);
 
+/* qamw_selftest_int8_gemm: qamw_int8_gemm whose copying and storing warps give up
+ *   at once where they wait for others (in the kernel for more than a few tokens;
+ *   that for a few has no waits).  It flags TIMEOUT, after a second at most, its
+ *   copies in flight land, and what it leaves in d_y is unspecified.  Errors: those of qamw_int8_gemm,
+ *   QAMW_ERR_INVALID for a null status. */
+QAMW_API int qamw_selftest_int8_gemm(const int8_t *d_x, const float *d_tok_scale, int ntok,
+                                     const int8_t *d_w, const float *d_row_scale, int d_out,
+                                     int d_in, void *d_y, int dtype, int32_t *d_status,
+                                     void *stream);
+
 /* ------------------------------------------------------------------ calls */
 
 /* Section 3.6 eq. (2): Lloyd iterations for the joint 2D codebook.
@@ -463,7 +473,7 @@ QAMW_API int qamw_rmsnorm_int8(const void *d_x, const void *d_residual, int dtyp
  *   d_x [ntok][d_in], 0 <= ntok <= 65536; d_w [d_out][d_in]; d_y [ntok][d_out]
  *   in dtype (QAMW_DTYPE_BF16 or _F32), rounded once from
  *   float(sum) * (tok_scale * row_scale).  The result does not depend on how
- *   the work is split.  Flags: TIMEOUT. */
+ *   the work is split.  Flags: TIMEOUT (d_y is unspecified then). */
 QAMW_API int qamw_int8_gemm(const int8_t *d_x, const float *d_tok_scale, int ntok,
                             const int8_t *d_w, const float *d_row_scale, int d_out, int d_in,
                             void *d_y, int dtype, int32_t *d_status, void *stream);

@@ -255,3 +255,23 @@ def test_products_whose_depth_clusters_share(ntok, d_out, d_in):
     for kind in ("bf16", "f32"):
         check_gemm(ints(ntok, d_in, 1, full=True), scales(ntok, 2), ints(d_out, d_in, 3, full=True),
                    scales(d_out, 4), T[kind])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("ntok,d_out,d_in", [(100, 256, 256), (16, 4096, 11008), (64, 2048, 4096), (200, 4096, 4096),
+                                             (300, 4096, 11008), (777, 5120, 2048), (2048, 9003, 1024)])
+def test_products_whose_waits_give_up(ntok, d_out, d_in, kind):
+    """Single CTAs, pairs and clusters whose roles give up at once: flagged, nothing written around
+    the outputs, and the calls after it (which need its tensor memory) are not affected."""
+    x, w, xs, ws = ints(ntok, d_in, 1), ints(d_out, d_in, 2), scales(ntok, 3), scales(d_out, 4)
+    want = check_gemm(x, xs, w, ws, T[kind])
+    buf = torch.full((ntok * d_out + 4096,), -7.0, dtype=T[kind], device=DEV)
+    y = buf[2048:2048 + ntok * d_out].view(ntok, d_out)
+    for _ in range(2):
+        st = status()
+        qamw.qamw_selftest_int8_gemm(x, xs, w, ws, y, st)
+        got = qamw.qamw_int8_gemm(x, xs, w, ws, dtype=T[kind])
+        torch.cuda.synchronize()
+        assert st.item() == qamw.QAMW_STATUS_TIMEOUT
+        assert (buf[:2048] == -7).all() and (buf[2048 + ntok * d_out:] == -7).all()
+        assert torch.equal(got, want)

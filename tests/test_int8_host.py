@@ -199,3 +199,10 @@ def test_a_refused_stream_leaves_the_device_as_it_was(monkeypatch):
         with pytest.raises((TypeError, ValueError)):
             qamw._enter(3, stream)
         assert not entered
+
+
+def test_giving_up_check_of_the_product_argument_errors():
+    S = L.qamw_selftest_int8_gemm
+    assert S(FAKE, FAKE, 4, FAKE, FAKE, 8, 128, FAKE, BF16, None, None) == INVALID
+    assert S(FAKE, FAKE, 4, FAKE, FAKE, 8, 100, FAKE, BF16, FAKE, None) == SHAPE
+    assert S(FAKE + 8, FAKE, 4, FAKE, FAKE, 8, 128, FAKE, BF16, FAKE, None) == ALIGN

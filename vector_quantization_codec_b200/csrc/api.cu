@@ -136,6 +136,22 @@ int rmsnorm_int8(unsigned tries, const void* d_x, const void* d_residual, int dt
                                      static_cast<cudaStream_t>(stream), tries));
 }
 
+int int8_gemm(unsigned tries, const int8_t* d_x, const float* d_tok_scale, int ntok,
+              const int8_t* d_w, const float* d_row_scale, int d_out, int d_in, void* d_y, int dtype,
+              int32_t* d_status, void* stream) {
+  if (dtype != QAMW_DTYPE_F32 && dtype != QAMW_DTYPE_BF16) return QAMW_ERR_INVALID;
+  if (d_out < 0 || d_out > kMaxInt8Rows || d_in <= 0 || d_in % kE != 0 || d_in > kMaxDin)
+    return QAMW_ERR_SHAPE;
+  if (ntok < 0 || ntok > kMaxTokens) return QAMW_ERR_INVALID;
+  if (ntok == 0 || d_out == 0) return QAMW_OK;
+  if (!d_x || !d_tok_scale || !d_w || !d_row_scale || !d_y) return QAMW_ERR_INVALID;
+  if (!aligned16(d_x) || !aligned16(d_w)) return QAMW_ERR_ALIGN;
+  if (!aligned(d_tok_scale, 4) || !aligned(d_row_scale, 4)) return QAMW_ERR_ALIGN;
+  if (!aligned(d_y, dtype == QAMW_DTYPE_F32 ? 4 : 2)) return QAMW_ERR_ALIGN;
+  return cuda_rc(launch_int8_gemm(d_x, d_tok_scale, ntok, d_w, d_row_scale, d_out, d_in, d_y, dtype,
+                                  d_status, static_cast<cudaStream_t>(stream), tries));
+}
+
 }  // namespace
 
 extern "C" {
@@ -477,17 +493,16 @@ int qamw_selftest_rmsnorm_int8(unsigned tries, const void* d_x, const void* d_re
 int qamw_int8_gemm(const int8_t* d_x, const float* d_tok_scale, int ntok, const int8_t* d_w,
                    const float* d_row_scale, int d_out, int d_in, void* d_y, int dtype,
                    int32_t* d_status, void* stream) {
-  if (dtype != QAMW_DTYPE_F32 && dtype != QAMW_DTYPE_BF16) return QAMW_ERR_INVALID;
-  if (d_out < 0 || d_out > kMaxInt8Rows || d_in <= 0 || d_in % kE != 0 || d_in > kMaxDin)
-    return QAMW_ERR_SHAPE;
-  if (ntok < 0 || ntok > kMaxTokens) return QAMW_ERR_INVALID;
-  if (ntok == 0 || d_out == 0) return QAMW_OK;
-  if (!d_x || !d_tok_scale || !d_w || !d_row_scale || !d_y) return QAMW_ERR_INVALID;
-  if (!aligned16(d_x) || !aligned16(d_w)) return QAMW_ERR_ALIGN;
-  if (!aligned(d_tok_scale, 4) || !aligned(d_row_scale, 4)) return QAMW_ERR_ALIGN;
-  if (!aligned(d_y, dtype == QAMW_DTYPE_F32 ? 4 : 2)) return QAMW_ERR_ALIGN;
-  return cuda_rc(launch_int8_gemm(d_x, d_tok_scale, ntok, d_w, d_row_scale, d_out, d_in, d_y, dtype,
-                                  d_status, static_cast<cudaStream_t>(stream)));
+  return int8_gemm(kSpinLimit, d_x, d_tok_scale, ntok, d_w, d_row_scale, d_out, d_in, d_y, dtype,
+                   d_status, stream);
+}
+
+int qamw_selftest_int8_gemm(const int8_t* d_x, const float* d_tok_scale, int ntok,
+                            const int8_t* d_w, const float* d_row_scale, int d_out, int d_in,
+                            void* d_y, int dtype, int32_t* d_status, void* stream) {
+  if (!d_status) return QAMW_ERR_INVALID;
+  return int8_gemm(0, d_x, d_tok_scale, ntok, d_w, d_row_scale, d_out, d_in, d_y, dtype, d_status,
+                   stream);
 }
 
 }  // extern "C"

@@ -72,6 +72,12 @@ struct Int8GemmArgs {
   int boxes;       // chunks per stage
   int staged;      // bf16 outputs leave by tensor stores (map_y)
   int splits;      // CTAs (a cluster) that share a tile's chunks; 1: persistent over tiles
+  // Polls of the waits of the copying thread and of the epilogue warps, kSpinLimit or 0
+  // (for the check of giving up; the MMA thread, whose waits are the ones that cost time,
+  // then runs into its limit).  Nothing between: the CTAs of a pair that gave up at
+  // different steps rely on the second that the limit takes for the copies of the one
+  // that went on to land.
+  unsigned tries;
 };
 
 __device__ __forceinline__ void put(float* y, int64_t at, float v) { y[at] = v; }
@@ -376,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = (int)(tile - m * a.tok_tiles) * a.nt + (CG == 2 ? (int)rank * (a.nt / 2) : 0);
         for (int c = c_lo; c < c_hi; c += a.boxes) {
           const int nb = min(a.boxes, c_hi - c);
-          if (u > 0 && !mbar_wait_bounded(&empty[s], (u - 1) & 1u)) {
+          if (u > 0 && !mbar_wait_bounded(&empty[s], (u - 1) & 1u, a.tries)) {
             ok = false;
             break;
           }
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // barriers have landed
       const int used = u > 0 ? S : s;
       for (int k = 0; k < used && ok; ++k)
-        ok = mbar_wait_bounded(&empty[k], (k < s ? u : u - 1) & 1u);
+        ok = mbar_wait_bounded(&empty[k], (k < s ? u : u - 1) & 1u, a.tries);
       if (!ok) {  // given up: the copies at least have to land (a pair's leader waits for both)
         flags |= QAMW_STATUS_TIMEOUT;
         if (CG == 1 || rank == 0)
@@ -510,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // one lane polls: 32 pollers a warp would slow the other roles' waits.  A
       // wait that gives up is not repeated; the warps still meet at the barriers.
-      const bool ok = !alive || lane != 0 || mbar_wait_bounded(&accfull[b], (uint32_t)(n >> 1) & 1u);
+      const bool ok =
+          !alive || lane != 0 || mbar_wait_bounded(&accfull[b], (uint32_t)(n >> 1) & 1u, a.tries);
       if (__any_sync(0xffffffffu, !ok)) {
         flags |= QAMW_STATUS_TIMEOUT;
         alive = false;
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the CTA's partial sums into its own shared memory (the stages are free:
     // every MMA that reads them is done), [token][channel]
     int* part = reinterpret_cast<int*>(smem);
-    const bool ok = lane != 0 || mbar_wait_bounded(&accfull[0], 0);
+    const bool ok = lane != 0 || mbar_wait_bounded(&accfull[0], 0, a.tries);
     if (__any_sync(0xffffffffu, !ok)) flags |= QAMW_STATUS_TIMEOUT;
     tc_fence_after();
     for (int c = 16 * (warp >> 2); c < a.nt; c += 32) {
@@ -821,7 +828,7 @@ cudaError_t run_gemm(const Int8Plan& p, const CUtensorMap& mw, const CUtensorMap
 
 cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
-                             int32_t* d_status, cudaStream_t stream) {
+                             int32_t* d_status, cudaStream_t stream, unsigned tries) {
   const FewTokens few = few_token_kernel(ntok, d_out, d_in);
   if (few != FewTokens::kNone)
     return launch_int8_gemv(d_x, d_x_scale, ntok, d_w, d_w_scale, d_out, d_in, d_y, dtype,
@@ -847,6 +854,7 @@ cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok
   a.stages = p.stages;
   a.boxes = p.boxes;
   a.splits = p.splits;
+  a.tries = tries;
   a.staged = p.staged;
   if (a.staged && !encode_out_map(&my, d_y, ntok, d_out)) return cudaErrorInvalidValue;
   if (dtype == QAMW_DTYPE_F32)

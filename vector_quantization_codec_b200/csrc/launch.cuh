@@ -129,8 +129,9 @@ cudaError_t launch_rmsnorm_int8(const void* d_x, const void* d_residual, int dty
 cudaError_t launch_int8_gemv(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
                              bool mma, cudaStream_t stream);
+// tries: polls of the copies' and the epilogue's waits, kSpinLimit (or 0, for the check of giving up).
 cudaError_t launch_int8_gemm(const int8_t* d_x, const float* d_x_scale, int ntok, const int8_t* d_w,
                              const float* d_w_scale, int d_out, int d_in, void* d_y, int dtype,
-                             int32_t* d_status, cudaStream_t stream);
+                             int32_t* d_status, cudaStream_t stream, unsigned tries);
 
 }  // namespace qamw

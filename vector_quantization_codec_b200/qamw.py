@@ -57,7 +57,7 @@ EXPORTS = ("qamw_row_bytes", "qamw_default_block", "qamw_bits_per_weight",
            "qamw_scalar_codebook", "qamw_encode_rows_scalar",
            "qamw_normalised_pairs", "qamw_selftest_wait_timeout", "qamw_int8_encode_weights",
            "qamw_int8_encode_tokens", "qamw_rmsnorm_int8", "qamw_int8_gemm",
-           "qamw_selftest_rmsnorm_int8")
+           "qamw_selftest_rmsnorm_int8", "qamw_selftest_int8_gemm")
 
 
 class QamwError(RuntimeError):
@@ -114,6 +114,7 @@ def _load() -> C.CDLL:
         "qamw_rmsnorm_int8": (I, [V, V, I, V, C.c_float, I, I, V, V, V, V, V, V]),
         "qamw_selftest_rmsnorm_int8": (I, [C.c_uint, V, V, I, V, C.c_float, I, I, V, V, V, V, V, V]),
         "qamw_int8_gemm": (I, [V, V, I, V, V, I, I, V, I, V, V]),
+        "qamw_selftest_int8_gemm": (I, [V, V, I, V, V, I, I, V, I, V, V]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -396,6 +397,14 @@ def qamw_selftest_rmsnorm_int8(tries: int, x: torch.Tensor, gain: torch.Tensor, 
     _check("qamw_selftest_rmsnorm_int8",
            _lib.qamw_selftest_rmsnorm_int8(tries, _p(x), _p(residual), _dtype_code(x), _p(gain), eps, rows, d,
                                            None, _p(sum_out), _p(q), _p(tok_scale), _p(status), _s(stream)))
+
+
+def qamw_selftest_int8_gemm(xq: torch.Tensor, tok_scale: torch.Tensor, wq: torch.Tensor, row_scale: torch.Tensor,
+                            y: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """qamw_int8_gemm (dense tensors of its types and shapes, on one GPU) whose waits give up at once."""
+    _check("qamw_selftest_int8_gemm",
+           _lib.qamw_selftest_int8_gemm(_p(xq), _p(tok_scale), xq.shape[0], _p(wq), _p(row_scale), wq.shape[0],
+                                        xq.shape[1], _p(y), _dtype_code(y), _p(status), _s(stream)))
 
 
 def qamw_decode(m: EncodedMatrix, out: torch.Tensor | None = None,
