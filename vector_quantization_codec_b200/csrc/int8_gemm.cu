@@ -11,11 +11,13 @@
 // token whatever d_out is.
 //
 // Measured (B200, back to back over weights larger than L2): 8192 tokens 4096 ->
-// 11008 222 us, 3.3 Pop/s, twice the bf16 rate of a library product (at the power
-// cap of a long loop 258 us, 2.9); 2048 tokens 65 us with the tensor pipe active
-// 82% of the time; 777 tokens 5120 -> 13824 43.6 us (2.5 Pop/s); 100 tokens 11008
+// 11008 227 us, 3.3 Pop/s, twice the bf16 rate of a library product (at the power
+// cap of a long loop 261 us, 2.8); 2048 tokens 62 us with the tensor pipe active
+// 82% of the time; 777 tokens 5120 -> 13824 44.1 us (2.5 Pop/s); 100 tokens 11008
 // -> 4096 14.3 us, where the weights' way from HBM takes 7 and the cluster's
-// partial sums 2.5; 16 tokens 4096 -> 11008 11.1 us (4.1 TB/s).
+// partial sums 2.5; 16 tokens 4096 -> 11008 11.3 us (4.1 TB/s).  Outputs that leave
+// by direct stores: 8192 tokens 4096 -> 11008 in fp32 289 us, bf16 4096 -> 11009
+// 283; 777 tokens 5120 -> 13824 in fp32 47.8, bf16 -> 13825 46.5.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -702,10 +704,11 @@ int clusters_at_once(int per) {
   return n;
 }
 
-// Estimated time (ns) of a plan, fitted to 360 measured (shape, plan) pairs.  Over
-// 28 shapes from 9 x 4096 -> 4096 to 8192 x 4096 -> 11008, with 750 plans measured on
-// the kernel as it is, the plan that it picks is within 6% of the fastest (mean 1%),
-// but for 16 x 4096 -> 2048 (10%: six CTAs a cluster, not four).  A chunk of a CTA
+// Estimated time (ns) of a plan, fitted to 360 measured (shape, plan) pairs when 32
+// tokens were staged a barrier.  Over 28 shapes from 9 x 4096 -> 4096 to 8192 x 4096
+// -> 11008, with 716 plans measured on the kernel as it is, the plan that it picks is
+// within 6% of the fastest (mean 1%), but for 16 x 4096 -> 2048 (10%: six CTAs a
+// cluster, not four).  A chunk of a CTA
 // costs the longest of its MMAs, its way through shared memory (128 channels and nt /
 // cg tokens) and a floor; the last tile's epilogue is not hidden, earlier ones are
 // unless the depth is short; sharing a tile's chunks among CTAs costs two cluster

@@ -17,11 +17,14 @@
 //
 // Every element is read once and kept on chip between the reduction and the
 // rounding, so large batches are bound by HBM (measured, B200: norm with residual
-// 8192 x 5120 bf16 46.7 us, 6.29 TB/s, 98% of a copy's rate; fp32 weights 4096 x
-// 11008 35.4 us, 6.37 TB/s; bf16 tokens 4001 x 13824 26.8 us, 6.19 TB/s), narrow
-// bf16 rows without a residual by instructions (weights 4096 x 4096 10.6 us, 4.8
-// TB/s: about 190 per warp and row of 16 elements a lane), and a few rows by the
-// chain of launch, load, reduction and store (1 x 4096 2.5 us).
+// 8192 x 5120 bf16 46.3 us, 6.35 TB/s, 99% of a copy's rate; fp32 96 us, 5.7 TB/s;
+// fp32 weights 4096 x 11008 35.5 us, 6.34 TB/s; bf16 tokens 4001 x 13824 26.7 us,
+// 6.20 TB/s), narrow bf16 rows without a residual by instructions (norm 8192 x 5120
+// 26.9 us, 4.7 TB/s, weights 4096 x 4096 9.8 us, 5.1 TB/s: about 190 per warp and row
+// of 16 elements a lane), and a few rows by the chain of launch, load, reduction and
+// store (1 x 4096 2.5 us).  Rows too long for the ring below (kDeepRow) have no
+// loads in flight between the reduction and the next row: 2000 x 28672 tokens bf16
+// 43 us, 4.0 TB/s, fp32 59 us, 4.9 TB/s, norm with residual bf16 91 us, 4.4 TB/s.
 #include <algorithm>
 #include <cfloat>
 
