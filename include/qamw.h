@@ -163,8 +163,8 @@ QAMW_API int qamw_selftest_rmsnorm_int8(unsigned tries, const void *d_x, const v
 /* qamw_selftest_int8_gemm: qamw_int8_gemm whose copying and storing warps give up
  *   at once where they wait for others (in the kernel for more than a few tokens;
  *   that for a few has no waits).  It flags TIMEOUT, after a second at most, its
- *   copies in flight land, and what it leaves in d_y is unspecified.  Errors: those of qamw_int8_gemm,
- *   QAMW_ERR_INVALID for a null status. */
+ *   copies in flight land, and what it leaves in d_y is unspecified.  Errors:
+ *   those of qamw_int8_gemm, QAMW_ERR_INVALID for a null status. */
 QAMW_API int qamw_selftest_int8_gemm(const int8_t *d_x, const float *d_tok_scale, int ntok,
                                      const int8_t *d_w, const float *d_row_scale, int d_out,
                                      int d_in, void *d_y, int dtype, int32_t *d_status,

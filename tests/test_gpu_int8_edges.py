@@ -257,6 +257,30 @@ def test_products_whose_depth_clusters_share(ntok, d_out, d_in):
                    scales(d_out, 4), T[kind])
 
 
+def test_checks_of_giving_up_refuse_what_does_not_fit():
+    x, gain = values(4, 128, "bf16", 1), torch.ones(128, dtype=torch.bfloat16, device=DEV)
+    q, scale, st = torch.empty((4, 128), dtype=torch.int8, device=DEV), torch.empty(4, device=DEV), status()
+    norm = qamw.qamw_selftest_rmsnorm_int8
+    for bad in ((x, gain[:64], None, q, scale, st), (x, gain, None, q[:3], scale, st), (x, gain, None, q, scale[:3], st),
+                (x, gain, None, q, scale, st.cpu()), (x[:, :64], gain[:64], None, q, scale, st), (x, gain, x, q, scale, st)):
+        with pytest.raises(ValueError):
+            norm(0, *bad)
+    with pytest.raises(ValueError):
+        norm(0, x, gain, x[:2], q, scale, st, residual=x)
+    w, y = ints(8, 128, 2), torch.empty((4, 8), device=DEV)
+    for bad in ((q, scale, w[:, :64], scales(8, 1), y, st), (q, scale[:3], w, scales(8, 1), y, st),
+                (q, scale, w, scales(7, 1), y, st), (q, scale, w, scales(8, 1), y[:3], st),
+                (q, scale, w, scales(8, 1), y.half(), st), (q, scale, w, scales(8, 1), y, st.float())):
+        with pytest.raises(ValueError):
+            qamw.qamw_selftest_int8_gemm(*bad)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    norm(64, x, gain, None, q, scale, st, stream=side)
+    side.synchronize()
+    want = qamw.qamw_rmsnorm_int8(x, gain)
+    assert st.item() == 0 and torch.equal(q, want[0]) and torch.equal(scale, want[1])
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("ntok,d_out,d_in", [(100, 256, 256), (16, 4096, 11008), (64, 2048, 4096), (200, 4096, 4096),
                                              (300, 4096, 11008), (777, 5120, 2048), (2048, 9003, 1024)])

@@ -201,6 +201,15 @@ def test_a_refused_stream_leaves_the_device_as_it_was(monkeypatch):
         assert not entered
 
 
+def test_giving_up_checks_refuse_tensors_that_are_not_on_a_gpu():
+    x, q, one = torch.zeros((2, 64)), torch.zeros((2, 64), dtype=torch.int8), torch.ones(2)
+    st = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        qamw.qamw_selftest_rmsnorm_int8(0, x, x[0], None, q, one, st)
+    with pytest.raises(ValueError):
+        qamw.qamw_selftest_int8_gemm(q, one, q, one, torch.zeros((2, 2)), st)
+
+
 def test_giving_up_check_of_the_product_argument_errors():
     S = L.qamw_selftest_int8_gemm
     assert S(FAKE, FAKE, 4, FAKE, FAKE, 8, 128, FAKE, BF16, None, None) == INVALID

@@ -388,25 +388,6 @@ def qamw_selftest_wait_timeout(tries: int, status: torch.Tensor, cycles: torch.T
            _lib.qamw_selftest_wait_timeout(tries, _p(status), _p(cycles), _s(stream)))
 
 
-def qamw_selftest_rmsnorm_int8(tries: int, x: torch.Tensor, gain: torch.Tensor, sum_out: torch.Tensor | None,
-                               q: torch.Tensor, tok_scale: torch.Tensor, status: torch.Tensor,
-                               eps: float = 1e-5, residual: torch.Tensor | None = None, stream=None) -> None:
-    """qamw_rmsnorm_int8 (dense tensors of its types and shapes, on one GPU) whose waits for rows give
-    up after `tries` polls."""
-    rows, d = x.shape
-    _check("qamw_selftest_rmsnorm_int8",
-           _lib.qamw_selftest_rmsnorm_int8(tries, _p(x), _p(residual), _dtype_code(x), _p(gain), eps, rows, d,
-                                           None, _p(sum_out), _p(q), _p(tok_scale), _p(status), _s(stream)))
-
-
-def qamw_selftest_int8_gemm(xq: torch.Tensor, tok_scale: torch.Tensor, wq: torch.Tensor, row_scale: torch.Tensor,
-                            y: torch.Tensor, status: torch.Tensor, stream=None) -> None:
-    """qamw_int8_gemm (dense tensors of its types and shapes, on one GPU) whose waits give up at once."""
-    _check("qamw_selftest_int8_gemm",
-           _lib.qamw_selftest_int8_gemm(_p(xq), _p(tok_scale), xq.shape[0], _p(wq), _p(row_scale), wq.shape[0],
-                                        xq.shape[1], _p(y), _dtype_code(y), _p(status), _s(stream)))
-
-
 def qamw_decode(m: EncodedMatrix, out: torch.Tensor | None = None,
                 status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Decoder of paper section 3.2 into a bf16 [d_out, d_in] tensor."""
@@ -704,3 +685,43 @@ def qamw_int8_gemm(xq: torch.Tensor, tok_scale: torch.Tensor, wq: torch.Tensor,
             ctx.close()
     _check("qamw_int8_gemm", rc)
     return y
+
+
+def qamw_selftest_rmsnorm_int8(tries: int, x: torch.Tensor, gain: torch.Tensor, sum_out: torch.Tensor | None,
+                               q: torch.Tensor, tok_scale: torch.Tensor, status: torch.Tensor,
+                               eps: float = 1e-5, residual: torch.Tensor | None = None, stream=None) -> None:
+    """qamw_rmsnorm_int8 whose waits for rows give up after `tries` polls: flags
+    QAMW_STATUS_TIMEOUT, and leaves the codes and scales of rows that it did not get to alone."""
+    code = _rows_of("x", x)
+    rows, d = x.shape
+    dev = x.get_device()
+    if (residual is None) != (sum_out is None):
+        raise ValueError("residual and sum_out come together")
+    args = (x.data_ptr(), None if residual is None else _dense("residual", residual, x.dtype, (rows, d), dev), code,
+            _dense("gain", gain, x.dtype, (d,), dev), eps, rows, d, None,
+            None if sum_out is None else _dense("sum_out", sum_out, x.dtype, (rows, d), dev),
+            _dense("q", q, torch.int8, (rows, d), dev), _dense("tok_scale", tok_scale, torch.float32, (rows,), dev),
+            _status_ptr(status, dev))
+    with _enter(dev, stream) or contextlib.nullcontext():
+        rc = _lib.qamw_selftest_rmsnorm_int8(tries, *args, _raw_stream(dev))
+        if stream is not None:
+            _used_on(dev, x, gain, sum_out, q, tok_scale, status, residual)
+    _check("qamw_selftest_rmsnorm_int8", rc)
+
+
+def qamw_selftest_int8_gemm(xq: torch.Tensor, tok_scale: torch.Tensor, wq: torch.Tensor, row_scale: torch.Tensor,
+                            y: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """qamw_int8_gemm whose waits give up at once: flags QAMW_STATUS_TIMEOUT, y is unspecified."""
+    if xq.dim() != 2 or wq.dim() != 2 or not xq.is_cuda or y.dtype not in _DTYPE_CODE:
+        raise ValueError("xq, wq: int8 [ntok, d_in] and [d_out, d_in] on a GPU; y: float32 or bfloat16")
+    ntok, d_in = xq.shape
+    d_out, dev = wq.shape[0], xq.get_device()
+    args = (_dense("xq", xq, torch.int8, (ntok, d_in), dev), _dense("tok_scale", tok_scale, torch.float32, (ntok,), dev),
+            ntok, _dense("wq", wq, torch.int8, (d_out, d_in), dev),
+            _dense("row_scale", row_scale, torch.float32, (d_out,), dev), d_out, d_in,
+            _dense("y", y, y.dtype, (ntok, d_out), dev), _DTYPE_CODE[y.dtype], _status_ptr(status, dev))
+    with _enter(dev, stream) or contextlib.nullcontext():
+        rc = _lib.qamw_selftest_int8_gemm(*args, _raw_stream(dev))
+        if stream is not None:
+            _used_on(dev, xq, tok_scale, wq, row_scale, y, status)
+    _check("qamw_selftest_int8_gemm", rc)
