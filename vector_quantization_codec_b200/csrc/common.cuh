@@ -48,8 +48,9 @@ __device__ __forceinline__ bool mask_negative(uint64_t seed, uint32_t j) {
 // its writes are visible (at once when there is no such kernel); every read of
 // data another path kernel writes (s, sigma, calibration partials, indices,
 // r_hat, x, W, the statistic) and every global write come after it.  Before it a
-// kernel reads only data no path kernel writes (the codebook, the search table).  pdl_trigger(), called after pdl_wait(), lets the next kernel start:
-// when kernel N starts, every kernel before N - 1 has completed.
+// kernel reads only data no path kernel writes (the codebook, the search table).
+// pdl_trigger(), called after pdl_wait(), lets the next kernel start: when kernel N
+// starts, every kernel before N - 1 has completed.
 // The 8-bit kernels' inputs may all come from the kernel ahead, which was still
 // running when they began.  After pdl_wait() they read them by ordinary loads or
 // from L2 (__ldcg), never by the read-only path (__ldg), which takes data to be
